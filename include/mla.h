@@ -486,6 +486,108 @@ mla_status mla_out_proj(const mla_config* cfg, const void* o_lat, const void* w_
                         const void* w_o, void* o, void* y, void* stream);
 
 /* --------------------------------------------------------------------------------------------
+ * The latent ring held in 4 bits.  The cache of a rollout is its standing memory (one ring per
+ * layer); this form keeps a token's D latents in D/2 + D/16 bytes (126 instead of 448 for the Wan
+ * widths).  d_c and d_rope must be multiples of 16 (else MLA_ERR_UNSUPPORTED).
+ *
+ *   codes   device uint8 [B, window_frames*tpf, D/2]   two 4-bit codes per byte, the even column
+ *                                                       in the low half; code c + 8, c in [-7, 7]
+ *   scales  device uint8 [B, window_frames*tpf, D/16]  one byte per 16 columns, E = byte / 8,
+ *                                                       M = byte mod 8: s = 2^(E-20) (1 + M/8)
+ *   value[col] = c[col] * s[col / 16], exact in bf16
+ * An empty ring holds zeros as codes 0x88 (c = 0); slot_frame is as for mla_cache_append.
+ *
+ * mla_cache_append_q4: mla_cache_append(MLA_APPEND) into such a ring.  Per group of 16 values the
+ *   scale is the smallest one >= max|x| / 7 and c = rint(x / s), so |x - c s| <= s / 2.  Values
+ *   beyond 26880 (7 times the largest scale) saturate; a NaN is stored as 0.
+ * mla_cache_read_q4: every row's values, cache device T [B, window_frames*tpf, D].
+ * mla_attention_fwd_q4, mla_attention_fwd_from_cq_q4: mla_attention_fwd and
+ *   mla_attention_fwd_from_cq over such a ring (every other argument, shape and error as there).
+ *   They equal those calls on the ring that mla_cache_read_q4 gives, bit for bit.  One pass decodes
+ *   the attended slots into the workspace and writes every rotated key; the attention follows.
+ *   Workspace: mla_attention_q4_workspace_bytes (0 for a bad configuration), 256-byte aligned; it
+ *   holds the attended slots as T values for the length of the call, so one serves every layer.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_ALIGNMENT, MLA_ERR_WORKSPACE,
+ * MLA_ERR_CUDA.
+ * ------------------------------------------------------------------------------------------ */
+mla_status mla_cache_append_q4(const mla_config* cfg, const void* chunk_lat, uint8_t* codes,
+                               uint8_t* scales, int32_t* slot_frame, int32_t first_frame,
+                               void* stream);
+mla_status mla_cache_read_q4(const mla_config* cfg, const uint8_t* codes, const uint8_t* scales,
+                             void* cache, void* stream);
+size_t mla_attention_q4_workspace_bytes(const mla_config* cfg, int32_t n_valid_frames);
+mla_status mla_attention_fwd_q4(const mla_config* cfg, const void* q, const void* chunk_lat,
+                                const uint8_t* codes, const uint8_t* scales,
+                                const int32_t* slot_frame, int32_t n_valid_frames,
+                                int32_t first_frame, const void* w_uv, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                void* stream);
+mla_status mla_attention_fwd_from_cq_q4(const mla_config* cfg, const void* c_q, const void* w_qcat,
+                                        const void* chunk_lat, const uint8_t* codes,
+                                        const uint8_t* scales, const int32_t* slot_frame,
+                                        int32_t n_valid_frames, int32_t first_frame,
+                                        const void* w_uv, void* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, int32_t* dev_status,
+                                        void* stream);
+
+/* --------------------------------------------------------------------------------------------
+ * Cross attention: the layer's other attention, of n_q tokens to the n_kv states of an encoder
+ * (text, image), with keys and values of their own, no rotation and no cache.
+ *
+ *   x[b,h,i,j] = softmax_scale * q[b,i,h] . k[b,j,h']     j < kv_len[b], h' = h / (H / H_kv)
+ *   out[b,i,h] = sum_j softmax_j(x) v[b,j,h'],  lse[b,h,i] = log sum_j exp(x)   (fp32)
+ *
+ *   q    device T [B, n_q, H, d_head]       k, v  device T [B, n_kv, H_kv, d_head]
+ *   out  device T [B, n_q, H, d_head]       lse   device float [B, H, n_q] or NULL
+ *   kv_len  device int32 [B] or NULL (every state valid): the first kv_len[b] states of sample b
+ *           are attended (clamped to [0, n_kv]); what the others hold is not used, be it NaN.
+ *           A sample with kv_len 0 gives out = 0 and lse = -infinity.
+ * q_row_stride, k_row_stride, v_row_stride: elements from one token to the next of q, k and v (0 =
+ * dense: H d_head or H_kv d_head), a multiple of 16 bytes and at least a token's heads; a sample's
+ * tokens follow one another (sample stride = tokens * row stride).  So q, k and v may be parts of
+ * the rows of one projection's output.  out and every gradient are dense.
+ *
+ * mla_cross_attention_bwd: the gradients of that call for the upstream gradient d_out (T, dense, as
+ * out), given the call's out and lse:
+ *   d_q as q, d_k and d_v as k and v (each summed over the query heads that share the key head;
+ *   rows past kv_len are zero).  A sample with kv_len 0 has zero gradients, one with kv_len 1 zero
+ *   d_q and d_k (its softmax is constant).
+ * Workspace: mla_cross_attention_bwd_workspace_bytes (0 for a bad configuration), 256-byte
+ * aligned.  Results do not depend on the order in which blocks run: the same call gives the same
+ * bits.
+ *
+ * dtype as in mla_config.  kernel_path: MLA_PATH_AUTO or MLA_PATH_SIMT (CUDA cores).  d_head <=
+ * 256.  Outputs must not overlap inputs.  dev_status as in mla_attention_fwd.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (d_head above 256), MLA_ERR_ALIGNMENT,
+ * MLA_ERR_WORKSPACE, MLA_ERR_CUDA.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct mla_cross_config {
+  int32_t batch;          /* B                                                             */
+  int32_t n_heads;        /* H query heads                                     (Wan: 12)   */
+  int32_t n_kv_heads;     /* H_kv key heads, a divisor of n_heads              (Wan: 12)   */
+  int32_t d_head;         /* per-head width of q, k, v and the output          (Wan: 128)  */
+  int32_t n_q;            /* query tokens per sample                                       */
+  int32_t n_kv;           /* encoder states per sample (the longest)                       */
+  float softmax_scale;    /* score scale, positive                                         */
+  int32_t dtype;          /* mla_dtype of every T array                                    */
+  int32_t kernel_path;    /* MLA_PATH_AUTO or MLA_PATH_SIMT                                */
+} mla_cross_config;
+
+/* Checks a cross-attention configuration without touching the device. */
+mla_status mla_cross_config_check(const mla_cross_config* cfg);
+mla_status mla_cross_attention_fwd(const mla_cross_config* cfg, const void* q, int64_t q_row_stride,
+                                   const void* k, int64_t k_row_stride, const void* v,
+                                   int64_t v_row_stride, const int32_t* kv_len, void* out,
+                                   float* lse, int32_t* dev_status, void* stream);
+size_t mla_cross_attention_bwd_workspace_bytes(const mla_cross_config* cfg);
+mla_status mla_cross_attention_bwd(const mla_cross_config* cfg, const void* q, int64_t q_row_stride,
+                                   const void* k, int64_t k_row_stride, const void* v,
+                                   int64_t v_row_stride, const int32_t* kv_len, const void* out,
+                                   const float* lse, const void* d_out, void* d_q, void* d_k,
+                                   void* d_v, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_status, void* stream);
+
+/* --------------------------------------------------------------------------------------------
  * mla_selftest_wait_timeout: checks, without faulting anything, that a kernel of this library
  * whose bounded wait runs out reports it.  It launches one thread that waits, with the same
  * bounded-wait routine the tensor-core kernels use, on a barrier that nothing ever completes;

@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from ctypes import c_float, c_int32, c_size_t, c_void_p, POINTER
+from ctypes import c_float, c_int32, c_int64, c_size_t, c_void_p, POINTER
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmla_b200.so")
 # the same library built with MLA_DEBUG (device-side contract checks; see include/mla.h)
@@ -49,9 +49,20 @@ class MLAConfigC(ctypes.Structure):
     ]
 
 
+class MLACrossConfigC(ctypes.Structure):
+    """Mirror of struct mla_cross_config."""
+
+    _fields_ = [
+        ("batch", c_int32), ("n_heads", c_int32), ("n_kv_heads", c_int32), ("d_head", c_int32),
+        ("n_q", c_int32), ("n_kv", c_int32), ("softmax_scale", c_float), ("dtype", c_int32),
+        ("kernel_path", c_int32),
+    ]
+
+
 _P = c_void_p
 _I32P = POINTER(c_int32)
 _CFG = POINTER(MLAConfigC)
+_CROSS = POINTER(MLACrossConfigC)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -89,6 +100,19 @@ SIGNATURES = {
                                                 _P, _P, c_size_t, _P, _P]),
     "mla_attention_fwd_static_scratch": (c_int32, [_CFG, _P, _P, _P, _P, c_int32, c_int32, _P,
                                                    _P, _P, _P, _P]),
+    "mla_cache_append_q4": (c_int32, [_CFG, _P, _P, _P, _P, c_int32, _P]),
+    "mla_cache_read_q4": (c_int32, [_CFG, _P, _P, _P, _P]),
+    "mla_attention_q4_workspace_bytes": (c_size_t, [_CFG, c_int32]),
+    "mla_attention_fwd_q4": (c_int32, [_CFG, _P, _P, _P, _P, _P, c_int32, c_int32, _P, _P, _P, _P,
+                                       c_size_t, _P, _P]),
+    "mla_attention_fwd_from_cq_q4": (c_int32, [_CFG, _P, _P, _P, _P, _P, _P, c_int32, c_int32, _P,
+                                               _P, _P, _P, c_size_t, _P, _P]),
+    "mla_cross_config_check": (c_int32, [_CROSS]),
+    "mla_cross_attention_fwd": (c_int32, [_CROSS, _P, c_int64, _P, c_int64, _P, c_int64, _P, _P,
+                                          _P, _P, _P]),
+    "mla_cross_attention_bwd_workspace_bytes": (c_size_t, [_CROSS]),
+    "mla_cross_attention_bwd": (c_int32, [_CROSS, _P, c_int64, _P, c_int64, _P, c_int64, _P, _P,
+                                          _P, _P, _P, _P, _P, _P, c_size_t, _P, _P]),
     "mla_selftest_wait_timeout": (c_int32, [_P, c_int32, _P]),
     "mla_selftest_exp2": (c_int32, [_P, _P, _P, _P, c_int32, _P]),
     "mla_selftest_sincos": (c_int32, [_P, _P, _P, c_int32, _P]),

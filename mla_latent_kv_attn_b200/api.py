@@ -7,13 +7,15 @@ status raises MLAError with the library's message.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+import math
+from typing import Optional, Tuple
 
 import torch
 
 from . import _lib
 from ._lib import (MLA_APPEND, MLA_BF16, MLA_FP32, MLA_PATH_AUTO, MLA_PATH_SIMT,
-                   MLA_PATH_TC_PAIR, MLA_PATH_TC_SINGLE, MLA_PROJECT, MLA_PROJECT_AND_APPEND, MLAConfigC, MLAError)
+                   MLA_PATH_TC_PAIR, MLA_PATH_TC_SINGLE, MLA_PROJECT, MLA_PROJECT_AND_APPEND, MLAConfigC, MLACrossConfigC,
+                   MLAError)
 
 __all__ = [
     "make_config", "torch_dtype", "mla_config_check", "mla_cache_append", "mla_rope3d",
@@ -22,7 +24,10 @@ __all__ = [
     "mla_project_latents", "mla_project_latents_rotated", "mla_attention_fwd_from_cq",
     "mla_rotate_ring_keys", "mla_attention_fwd_cached_ring", "mla_attention_uses_tensor_cores",
     "mla_attention_bwd_workspace_bytes", "mla_attention_bwd",
-    "mla_out_proj", "MLAError",
+    "mla_out_proj", "mla_cache_append_q4", "mla_cache_read_q4", "mla_attention_q4_workspace_bytes",
+    "mla_attention_fwd_q4", "mla_attention_fwd_from_cq_q4", "make_cross_config",
+    "mla_cross_config_check", "mla_cross_attention_fwd", "mla_cross_attention_bwd_workspace_bytes",
+    "mla_cross_attention_bwd", "MLAError",
     "MLA_PROJECT", "MLA_APPEND", "MLA_PROJECT_AND_APPEND", "MLA_PATH_AUTO", "MLA_PATH_SIMT",
     "MLA_PATH_TC_SINGLE", "MLA_PATH_TC_PAIR",
 ]
@@ -318,3 +323,160 @@ def mla_attention_fwd_static_scratch(c: MLAConfigC, q, chunk_lat, cache, slot_fr
         _ptr(lse, "lse", torch.float32, (B, H, n_q)), _ptr(dev_status, "dev_status", torch.int32),
         _stream(stream))
     _lib.check("mla_attention_fwd_static_scratch", st)
+
+
+# ---- the latent ring held in 4 bits -----------------------------------------------------------
+
+
+def _q4_ring(c: MLAConfigC, codes, scales):
+    tpf, _, D = _geom(c)
+    rows = (c.batch, c.window_frames * tpf)
+    return (_ptr(codes, "codes", torch.uint8, (*rows, D // 2)),
+            _ptr(scales, "scales", torch.uint8, (*rows, D // 16)))
+
+
+def mla_cache_append_q4(c: MLAConfigC, chunk_lat, codes, scales, slot_frame, first_frame: int,
+                        stream=None) -> None:
+    tpf, n_q, D = _geom(c)
+    st = _lib.lib().mla_cache_append_q4(
+        ctypes.byref(c), _ptr(chunk_lat, "chunk_lat", torch_dtype(c), (c.batch, n_q, D)),
+        *_q4_ring(c, codes, scales),
+        _ptr(slot_frame, "slot_frame", torch.int32, (c.batch, c.window_frames)), first_frame,
+        _stream(stream))
+    _lib.check("mla_cache_append_q4", st)
+
+
+def mla_cache_read_q4(c: MLAConfigC, codes, scales, cache, stream=None) -> None:
+    tpf, _, D = _geom(c)
+    st = _lib.lib().mla_cache_read_q4(
+        ctypes.byref(c), *_q4_ring(c, codes, scales),
+        _ptr(cache, "cache", torch_dtype(c), (c.batch, c.window_frames * tpf, D)), _stream(stream))
+    _lib.check("mla_cache_read_q4", st)
+
+
+def mla_attention_q4_workspace_bytes(c: MLAConfigC, n_valid_frames: int) -> int:
+    return int(_lib.lib().mla_attention_q4_workspace_bytes(ctypes.byref(c), n_valid_frames))
+
+
+def _attention_q4(fn_name: str, c: MLAConfigC, query, chunk_lat, codes, scales, slot_frame,
+                  n_valid_frames: int, first_frame: int, w_uv, out, lse, workspace, dev_status,
+                  stream) -> None:
+    tpf, n_q, D = _geom(c)
+    dt = torch_dtype(c)
+    B, H = c.batch, c.n_heads
+    out_shape = (B, n_q, H * c.d_head) if w_uv is not None else (B, n_q, H, c.d_c)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = getattr(_lib.lib(), fn_name)(
+        ctypes.byref(c), *query, _ptr(chunk_lat, "chunk_lat", dt, (B, n_q, D)),
+        *_q4_ring(c, codes, scales),
+        _ptr(slot_frame, "slot_frame", torch.int32, (B, c.window_frames)), n_valid_frames,
+        first_frame, _ptr(w_uv, "w_uv", dt, (H, c.d_head, c.d_c)), _ptr(out, "out", dt, out_shape),
+        _ptr(lse, "lse", torch.float32, (B, H, n_q)), _ptr(workspace, "workspace"), ws_bytes,
+        _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
+    _lib.check(fn_name, st)
+
+
+def mla_attention_fwd_q4(c: MLAConfigC, q, chunk_lat, codes, scales, slot_frame,
+                         n_valid_frames: int, first_frame: int, w_uv, out, lse=None,
+                         workspace=None, dev_status=None, stream=None) -> None:
+    """mla_attention_fwd over a ring held in 4 bits."""
+    _, n_q, D = _geom(c)
+    query = (_ptr(q, "q", torch_dtype(c), (c.batch, n_q, c.n_heads, D)),)
+    _attention_q4("mla_attention_fwd_q4", c, query, chunk_lat, codes, scales, slot_frame,
+                  n_valid_frames, first_frame, w_uv, out, lse, workspace, dev_status, stream)
+
+
+def mla_attention_fwd_from_cq_q4(c: MLAConfigC, c_q, w_qcat, chunk_lat, codes, scales, slot_frame,
+                                 n_valid_frames: int, first_frame: int, w_uv, out, lse=None,
+                                 workspace=None, dev_status=None, stream=None) -> None:
+    """mla_attention_fwd_from_cq over a ring held in 4 bits."""
+    _, n_q, D = _geom(c)
+    dt = torch_dtype(c)
+    query = (_ptr(c_q, "c_q", dt, (c.batch, n_q, c.d_cq)),
+             _ptr(w_qcat, "w_qcat", dt, (c.n_heads, D, c.d_cq)))
+    _attention_q4("mla_attention_fwd_from_cq_q4", c, query, chunk_lat, codes, scales, slot_frame,
+                  n_valid_frames, first_frame, w_uv, out, lse, workspace, dev_status, stream)
+
+
+# ---- cross attention to an encoder's states ---------------------------------------------------
+
+
+def make_cross_config(batch: int, n_heads: int, d_head: int, n_q: int, n_kv: int,
+                      n_kv_heads: Optional[int] = None, softmax_scale: Optional[float] = None,
+                      dtype: str = "bf16", kernel_path: int = MLA_PATH_AUTO) -> MLACrossConfigC:
+    """struct mla_cross_config; softmax_scale defaults to 1/sqrt(d_head), n_kv_heads to n_heads."""
+    if dtype not in ("bf16", "fp32"):
+        raise ValueError(f"unknown dtype {dtype!r}")
+    return MLACrossConfigC(
+        batch=batch, n_heads=n_heads, n_kv_heads=n_heads if n_kv_heads is None else n_kv_heads,
+        d_head=d_head, n_q=n_q, n_kv=n_kv,
+        softmax_scale=1.0 / math.sqrt(d_head) if softmax_scale is None else softmax_scale,
+        dtype=MLA_FP32 if dtype == "fp32" else MLA_BF16, kernel_path=kernel_path)
+
+
+def mla_cross_config_check(cc: MLACrossConfigC) -> None:
+    _lib.check("mla_cross_config_check", _lib.lib().mla_cross_config_check(ctypes.byref(cc)))
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape) -> Tuple[int, int]:
+    """Pointer and row stride of a [B, n, H, d] tensor whose tokens' heads are dense and whose
+    samples' tokens follow one another (a dense tensor, or part of the rows of one)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    B, n, H, d = shape
+    sb, sn, sh, sd = t.stride()
+    row = sn if n > 1 else sb if B > 1 else H * d      # (the stride of a dimension of 1 says nothing)
+    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (B > 1 and sb != n * row) or row < H * d:
+        raise ValueError(f"{name} must have dense heads and tokens at one stride: got strides "
+                         f"{t.stride()} for shape {tuple(t.shape)}")
+    return t.data_ptr(), row
+
+
+def _cross_dtype(cc: MLACrossConfigC) -> torch.dtype:
+    return torch.float32 if cc.dtype == MLA_FP32 else torch.bfloat16
+
+
+def _cross_inputs(cc: MLACrossConfigC, q, k, v, kv_len):
+    dt = _cross_dtype(cc)
+    kv = (cc.batch, cc.n_kv, cc.n_kv_heads, cc.d_head)
+    return (*_rows(q, "q", dt, (cc.batch, cc.n_q, cc.n_heads, cc.d_head)), *_rows(k, "k", dt, kv),
+            *_rows(v, "v", dt, kv), _ptr(kv_len, "kv_len", torch.int32, (cc.batch,)))
+
+
+def mla_cross_attention_fwd(cc: MLACrossConfigC, q, k, v, out, lse=None, kv_len=None,
+                            dev_status=None, stream=None) -> None:
+    """Attention of q [B, n_q, H, d] to the first kv_len[b] of an encoder's states k, v
+    [B, n_kv, H_kv, d].  q, k and v may be parts of wider rows (see include/mla.h)."""
+    dt = _cross_dtype(cc)
+    st = _lib.lib().mla_cross_attention_fwd(
+        ctypes.byref(cc), *_cross_inputs(cc, q, k, v, kv_len),
+        _ptr(out, "out", dt, (cc.batch, cc.n_q, cc.n_heads, cc.d_head)),
+        _ptr(lse, "lse", torch.float32, (cc.batch, cc.n_heads, cc.n_q)),
+        _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
+    _lib.check("mla_cross_attention_fwd", st)
+
+
+def mla_cross_attention_bwd_workspace_bytes(cc: MLACrossConfigC) -> int:
+    return int(_lib.lib().mla_cross_attention_bwd_workspace_bytes(ctypes.byref(cc)))
+
+
+def mla_cross_attention_bwd(cc: MLACrossConfigC, q, k, v, out, lse, d_out, d_q, d_k, d_v,
+                            workspace, kv_len=None, dev_status=None, stream=None) -> None:
+    """Gradients of mla_cross_attention_fwd, given its out and lse (see include/mla.h)."""
+    dt = _cross_dtype(cc)
+    rows = (cc.batch, cc.n_q, cc.n_heads, cc.d_head)
+    kv = (cc.batch, cc.n_kv, cc.n_kv_heads, cc.d_head)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = _lib.lib().mla_cross_attention_bwd(
+        ctypes.byref(cc), *_cross_inputs(cc, q, k, v, kv_len), _ptr(out, "out", dt, rows),
+        _ptr(lse, "lse", torch.float32, (cc.batch, cc.n_heads, cc.n_q)),
+        _ptr(d_out, "d_out", dt, rows), _ptr(d_q, "d_q", dt, rows), _ptr(d_k, "d_k", dt, kv),
+        _ptr(d_v, "d_v", dt, kv), _ptr(workspace, "workspace"), ws_bytes,
+        _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
+    _lib.check("mla_cross_attention_bwd", st)

@@ -5,7 +5,9 @@
 #include <cstring>
 #include <string>
 
+#include "cross.h"
 #include "kernels.h"
+#include "ring_q4.h"
 
 namespace mla {
 
@@ -187,6 +189,15 @@ mla_status check_workspace(const Dims& d, int n_valid, const void* workspace,
   return check_ptr(workspace, "workspace");
 }
 
+// A workspace of which `need` bytes are used.
+mla_status check_scratch(const void* workspace, size_t workspace_bytes, size_t need) {
+  if (workspace == nullptr || workspace_bytes < need)
+    MLA_FAIL(MLA_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    MLA_FAIL(MLA_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  return check_ptr(workspace, "workspace");
+}
+
 // project_latents plus the rotated positional keys of the chunk's attention in the key
 // workspace: on the tensor cores one GEMM whose epilogue writes them (the ring's too with
 // rotate_ring), otherwise the GEMMs and the rotation pass.
@@ -289,6 +300,124 @@ mla_status attention_from_cq_entry(const mla_config* cfg, const void* c_q, const
   a.q = nullptr; a.chunk_lat = chunk_lat; a.cache = cache; a.ws = workspace; a.w_uv = w_uv;
   a.out = out; a.lse = lse; a.dev_status = dev_status;
   return attention_tc_fused_q(d, a, n_valid_frames, c_q, w_qcat, first_frame, s);
+}
+
+// The 4-bit ring needs whole groups of content and of positional values.
+mla_status check_q4(const Dims& d, const void* codes, const void* scales) {
+  if (d.d_c % kQ4Group != 0 || d.d_rope % kQ4Group != 0)
+    MLA_FAIL(MLA_ERR_UNSUPPORTED, "the 4-bit ring needs d_c (%d) and d_rope (%d) in multiples of %d",
+             d.d_c, d.d_rope, kQ4Group);
+  MLA_TRY(check_ptr(codes, "codes"));
+  return check_ptr(scales, "scales");
+}
+
+// Shared body of the attention entry points over the 4-bit ring: checks, the pass that decodes the
+// ring's content and writes every rotated key, and the attention kernel over its result.
+mla_status attention_q4_entry(const mla_config* cfg, const void* q, const void* c_q,
+                              const void* w_qcat, const void* chunk_lat, const uint8_t* codes,
+                              const uint8_t* scales, const int32_t* slot_frame,
+                              int32_t n_valid_frames, int32_t first_frame, const void* w_uv,
+                              void* out, float* lse, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream, bool from_cq) {
+  set_last_error("");
+  MLA_TRY(check_cfg(cfg));
+  const Dims d = dims_of(*cfg);
+  MLA_CHECK_ARG(n_valid_frames >= 0 && n_valid_frames <= d.W, "n_valid_frames must be in [0, %d]",
+                d.W);
+  MLA_TRY(check_first_frame(first_frame, d.C));
+  if (from_cq && !(use_tc(d) && tc_attention_fused_q_supported(d, w_uv != nullptr)))
+    MLA_FAIL(MLA_ERR_UNSUPPORTED,
+             "attention from the query latent needs the tensor-core path (bf16, d_c <= 192, "
+             "d_c + d_rope <= 256, d_cq a multiple of 64); use mla_project_chunk and "
+             "mla_attention_fwd_q4");
+  MLA_TRY(check_q4(d, codes, scales));
+  if (from_cq) {
+    MLA_TRY(check_ptr(c_q, "c_q"));
+    MLA_TRY(check_ptr(w_qcat, "w_qcat"));
+  } else {
+    MLA_TRY(check_ptr(q, "q"));
+  }
+  MLA_TRY(check_ptr(chunk_lat, "chunk_lat"));
+  MLA_TRY(check_ptr(slot_frame, "slot_frame"));
+  MLA_TRY(check_ptr(out, "out"));
+  MLA_TRY(check_ptr(w_uv, "w_uv", false));
+  MLA_TRY(check_ptr(lse, "lse", false));
+  MLA_TRY(check_ptr(dev_status, "dev_status", false));
+  const Q4Workspace w = q4_workspace_layout(d, n_valid_frames);
+  MLA_TRY(check_scratch(workspace, workspace_bytes, w.bytes));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* ring = static_cast<char*>(workspace) + w.key_bytes;
+  MLA_TRY(q4_prepare(d, codes, scales, chunk_lat, slot_frame, n_valid_frames, first_frame, ring,
+                     workspace, dev_status, s));
+  // the decoded rows of a sample follow one another: a ring of n_valid_frames slots
+  Dims dr = d;
+  dr.W = n_valid_frames;
+  AttnArgs a{};
+  a.q = q; a.chunk_lat = chunk_lat; a.cache = ring; a.ws = workspace; a.w_uv = w_uv;
+  a.out = out; a.lse = lse; a.dev_status = dev_status;
+  if (from_cq) return attention_tc_fused_q(dr, a, n_valid_frames, c_q, w_qcat, first_frame, s);
+  return attention_dispatch(dr, a, n_valid_frames, s);
+}
+
+// ---- cross attention to an encoder's states ---------------------------------------------------
+
+mla_status check_cross_cfg(const mla_cross_config* cfg) {
+  MLA_CHECK_ARG(cfg != nullptr, "config is null");
+  const mla_cross_config& c = *cfg;
+  MLA_CHECK_ARG(c.batch > 0 && c.n_heads > 0 && c.n_kv_heads > 0 && c.d_head > 0 && c.n_q > 0 &&
+                    c.n_kv > 0,
+                "batch, head counts, d_head, n_q and n_kv must be positive");
+  MLA_CHECK_ARG(c.n_heads % c.n_kv_heads == 0, "n_heads (%d) must be a multiple of n_kv_heads (%d)",
+                c.n_heads, c.n_kv_heads);
+  MLA_CHECK_ARG(std::isfinite(c.softmax_scale) && c.softmax_scale > 0.f,
+                "softmax_scale must be positive and finite");
+  MLA_CHECK_ARG(c.dtype == MLA_BF16 || c.dtype == MLA_FP32, "unknown dtype %d", c.dtype);
+  MLA_CHECK_ARG(c.kernel_path == MLA_PATH_AUTO || c.kernel_path == MLA_PATH_SIMT,
+                "kernel_path must be MLA_PATH_AUTO or MLA_PATH_SIMT");
+  MLA_CHECK_ARG(c.n_heads <= 65535 && c.batch <= 65535, "at most 65535 heads and samples");
+  if (c.d_head > kCrossMaxD)
+    MLA_FAIL(MLA_ERR_UNSUPPORTED, "d_head (%d) above %d", c.d_head, kCrossMaxD);
+  const int64_t q = int64_t{c.n_heads} * c.d_head, kv = int64_t{c.n_kv_heads} * c.d_head;
+  MLA_CHECK_ARG(int64_t{c.batch} * c.n_q < kMaxElems / q && int64_t{c.batch} * c.n_kv < kMaxElems / kv,
+                "workload too large: every array must hold fewer than 2^31 elements");
+  return MLA_OK;
+}
+
+// A row stride in elements: 0 stands for dense rows; rows start on 16 bytes and do not overlap.
+mla_status check_row_stride(int64_t given, int64_t dense, int64_t rows, int dtype, const char* name,
+                            int64_t* stride) {
+  *stride = given == 0 ? dense : given;
+  MLA_CHECK_ARG(*stride >= dense, "%s row stride (%lld) below a row's %lld elements", name,
+                static_cast<long long>(given), static_cast<long long>(dense));
+  MLA_CHECK_ARG(*stride < kMaxElems && rows < kMaxElems / *stride,
+                "%s spans 2^31 elements or more", name);
+  if (given != 0 && (given * static_cast<int64_t>(dtype_size(dtype))) % 16 != 0)
+    MLA_FAIL(MLA_ERR_ALIGNMENT, "%s row stride (%lld elements) is not a multiple of 16 bytes", name,
+             static_cast<long long>(given));
+  return MLA_OK;
+}
+
+mla_status cross_dims(const mla_cross_config* cfg, int64_t q_row, int64_t k_row, int64_t v_row,
+                      CrossDims* d) {
+  MLA_TRY(check_cross_cfg(cfg));
+  const mla_cross_config& c = *cfg;
+  d->B = c.batch; d->H = c.n_heads; d->Hkv = c.n_kv_heads; d->d = c.d_head; d->n_q = c.n_q;
+  d->n_kv = c.n_kv; d->scale = c.softmax_scale; d->dtype = c.dtype; d->path = c.kernel_path;
+  const int64_t qw = int64_t{c.n_heads} * c.d_head, kw = int64_t{c.n_kv_heads} * c.d_head;
+  MLA_TRY(check_row_stride(q_row, qw, int64_t{c.batch} * c.n_q, c.dtype, "q", &d->q_row));
+  MLA_TRY(check_row_stride(k_row, kw, int64_t{c.batch} * c.n_kv, c.dtype, "k", &d->k_row));
+  return check_row_stride(v_row, kw, int64_t{c.batch} * c.n_kv, c.dtype, "v", &d->v_row);
+}
+
+struct CrossBwdWorkspace {
+  size_t delta_bytes, bytes;
+};
+
+CrossBwdWorkspace cross_bwd_workspace_layout(const mla_cross_config& c) {
+  CrossBwdWorkspace w;
+  w.delta_bytes = (static_cast<size_t>(c.batch) * c.n_heads * c.n_q * sizeof(float) + 255) / 256 * 256;
+  w.bytes = w.delta_bytes;
+  return w;
 }
 
 }  // namespace
@@ -697,6 +826,124 @@ mla_status mla_out_proj(const mla_config* cfg, const void* o_lat, const void* w_
     MLA_TRY(gemm(d, o, int64_t{d.H} * d.d_head, 0, w_o, int64_t{d.H} * d.d_head, 0, y, d.d_model, 0,
                  M, d.d_model, d.H * d.d_head, 1, s));
   return MLA_OK;
+}
+
+mla_status mla_cache_append_q4(const mla_config* cfg, const void* chunk_lat, uint8_t* codes,
+                               uint8_t* scales, int32_t* slot_frame, int32_t first_frame,
+                               void* stream) {
+  MLA_NVTX_RANGE("mla_cache_append_q4");
+  set_last_error("");
+  MLA_TRY(check_cfg(cfg));
+  const Dims d = dims_of(*cfg);
+  MLA_TRY(check_first_frame(first_frame, d.C));
+  MLA_TRY(check_q4(d, codes, scales));
+  MLA_TRY(check_ptr(chunk_lat, "chunk_lat"));
+  MLA_TRY(check_ptr(slot_frame, "slot_frame"));
+  return q4_append(d, chunk_lat, codes, scales, slot_frame, first_frame,
+                   static_cast<cudaStream_t>(stream));
+}
+
+mla_status mla_cache_read_q4(const mla_config* cfg, const uint8_t* codes, const uint8_t* scales,
+                             void* cache, void* stream) {
+  MLA_NVTX_RANGE("mla_cache_read_q4");
+  set_last_error("");
+  MLA_TRY(check_cfg(cfg));
+  const Dims d = dims_of(*cfg);
+  MLA_TRY(check_q4(d, codes, scales));
+  MLA_TRY(check_ptr(cache, "cache"));
+  return q4_read(d, codes, scales, d.W * d.tpf, cache, static_cast<cudaStream_t>(stream));
+}
+
+size_t mla_attention_q4_workspace_bytes(const mla_config* cfg, int32_t n_valid_frames) {
+  if (check_cfg(cfg) != MLA_OK) return 0;
+  const Dims d = dims_of(*cfg);
+  if (n_valid_frames < 0 || n_valid_frames > d.W) return 0;
+  return q4_workspace_layout(d, n_valid_frames).bytes;
+}
+
+mla_status mla_attention_fwd_q4(const mla_config* cfg, const void* q, const void* chunk_lat,
+                                const uint8_t* codes, const uint8_t* scales,
+                                const int32_t* slot_frame, int32_t n_valid_frames,
+                                int32_t first_frame, const void* w_uv, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                void* stream) {
+  MLA_NVTX_RANGE("mla_attention_fwd_q4");
+  return attention_q4_entry(cfg, q, nullptr, nullptr, chunk_lat, codes, scales, slot_frame,
+                            n_valid_frames, first_frame, w_uv, out, lse, workspace,
+                            workspace_bytes, dev_status, stream, false);
+}
+
+mla_status mla_attention_fwd_from_cq_q4(const mla_config* cfg, const void* c_q, const void* w_qcat,
+                                        const void* chunk_lat, const uint8_t* codes,
+                                        const uint8_t* scales, const int32_t* slot_frame,
+                                        int32_t n_valid_frames, int32_t first_frame,
+                                        const void* w_uv, void* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, int32_t* dev_status,
+                                        void* stream) {
+  MLA_NVTX_RANGE("mla_attention_fwd_from_cq_q4");
+  return attention_q4_entry(cfg, nullptr, c_q, w_qcat, chunk_lat, codes, scales, slot_frame,
+                            n_valid_frames, first_frame, w_uv, out, lse, workspace,
+                            workspace_bytes, dev_status, stream, true);
+}
+
+mla_status mla_cross_config_check(const mla_cross_config* cfg) {
+  MLA_NVTX_RANGE("mla_cross_config_check");
+  set_last_error("");
+  return check_cross_cfg(cfg);
+}
+
+mla_status mla_cross_attention_fwd(const mla_cross_config* cfg, const void* q, int64_t q_row_stride,
+                                   const void* k, int64_t k_row_stride, const void* v,
+                                   int64_t v_row_stride, const int32_t* kv_len, void* out,
+                                   float* lse, int32_t* dev_status, void* stream) {
+  MLA_NVTX_RANGE("mla_cross_attention_fwd");
+  set_last_error("");
+  CrossDims d;
+  MLA_TRY(cross_dims(cfg, q_row_stride, k_row_stride, v_row_stride, &d));
+  MLA_TRY(check_ptr(q, "q"));
+  MLA_TRY(check_ptr(k, "k"));
+  MLA_TRY(check_ptr(v, "v"));
+  MLA_TRY(check_ptr(kv_len, "kv_len", false));
+  MLA_TRY(check_ptr(out, "out"));
+  MLA_TRY(check_ptr(lse, "lse", false));
+  MLA_TRY(check_ptr(dev_status, "dev_status", false));
+  CrossArgs a{};
+  a.q = q; a.k = k; a.v = v; a.kv_len = kv_len; a.out = out; a.lse = lse; a.dev_status = dev_status;
+  return cross_fwd_simt(d, a, static_cast<cudaStream_t>(stream));
+}
+
+size_t mla_cross_attention_bwd_workspace_bytes(const mla_cross_config* cfg) {
+  if (check_cross_cfg(cfg) != MLA_OK) return 0;
+  return cross_bwd_workspace_layout(*cfg).bytes;
+}
+
+mla_status mla_cross_attention_bwd(const mla_cross_config* cfg, const void* q, int64_t q_row_stride,
+                                   const void* k, int64_t k_row_stride, const void* v,
+                                   int64_t v_row_stride, const int32_t* kv_len, const void* out,
+                                   const float* lse, const void* d_out, void* d_q, void* d_k,
+                                   void* d_v, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_status, void* stream) {
+  MLA_NVTX_RANGE("mla_cross_attention_bwd");
+  set_last_error("");
+  CrossDims d;
+  MLA_TRY(cross_dims(cfg, q_row_stride, k_row_stride, v_row_stride, &d));
+  MLA_TRY(check_ptr(q, "q"));
+  MLA_TRY(check_ptr(k, "k"));
+  MLA_TRY(check_ptr(v, "v"));
+  MLA_TRY(check_ptr(kv_len, "kv_len", false));
+  MLA_TRY(check_ptr(out, "out"));
+  MLA_TRY(check_ptr(lse, "lse"));
+  MLA_TRY(check_ptr(d_out, "d_out"));
+  MLA_TRY(check_ptr(d_q, "d_q"));
+  MLA_TRY(check_ptr(d_k, "d_k"));
+  MLA_TRY(check_ptr(d_v, "d_v"));
+  MLA_TRY(check_ptr(dev_status, "dev_status", false));
+  const CrossBwdWorkspace w = cross_bwd_workspace_layout(*cfg);
+  MLA_TRY(check_scratch(workspace, workspace_bytes, w.bytes));
+  CrossBwdArgs a{};
+  a.q = q; a.k = k; a.v = v; a.kv_len = kv_len; a.out = out; a.lse = lse; a.d_out = d_out;
+  a.d_q = d_q; a.d_k = d_k; a.d_v = d_v; a.dev_status = dev_status;
+  return cross_bwd_simt(d, a, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,32 @@
+// ring_q4.h - internal launchers of the 4-bit latent ring (ring_q4.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace mla {
+
+constexpr int kQ4Group = 16;   // values that share a scale
+
+// Workspace of an attention call over the 4-bit ring: the rotated keys (as the attention over a
+// T ring has them), then the decoded ring rows [B, n_valid * tpf, D].
+struct Q4Workspace {
+  size_t key_bytes, ring_bytes, bytes;
+};
+Q4Workspace q4_workspace_layout(const Dims& d, int n_valid);
+
+// chunk_lat [B, n_q, D] into the slots of frames first_frame .. first_frame + C - 1.
+mla_status q4_append(const Dims& d, const void* chunk_lat, uint8_t* codes, uint8_t* scales,
+                     int32_t* slot_frame, int first_frame, cudaStream_t s);
+// The first `rows` rows of every sample's ring as T values, out [B, rows, D].
+mla_status q4_read(const Dims& d, const uint8_t* codes, const uint8_t* scales, int rows, void* out,
+                   cudaStream_t s);
+// The attention's inputs from the 4-bit ring: the content columns of the first n_valid * tpf rows
+// into ring [B, n_valid * tpf, D], and every rotated positional key into ws.
+mla_status q4_prepare(const Dims& d, const uint8_t* codes, const uint8_t* scales,
+                      const void* chunk_lat, const int32_t* slot_frame, int n_valid,
+                      int first_frame, void* ring, void* ws, int32_t* dev_status, cudaStream_t s);
+
+}  // namespace mla

@@ -72,10 +72,44 @@ class Ring:
         self.slot_frame.copy_(sd["slot_frame"])
 
 
-class ChunkBuffers:
-    """Per-chunk activations and scratch, allocated once per workload."""
+class RingQ4:
+    """The latent cache of one layer held in 4 bits: codes [B, W*tpf, D/2], scales [B, W*tpf, D/16]
+    and slot_frame [B, W] (include/mla.h).  It takes the place of a Ring in every function below;
+    the chunk's buffers must be made with q4=True."""
 
-    def __init__(self, c, device="cuda", fuse_uv: bool = True):
+    def __init__(self, c, device="cuda"):
+        tpf = c.frame_h * c.frame_w
+        D = c.d_c + c.d_rope
+        self.c = c
+        rows = (c.batch, c.window_frames * tpf)
+        # 0x88: two codes of value zero
+        self.codes = torch.full((*rows, D // 2), 0x88, device=device, dtype=torch.uint8)
+        self.scales = torch.zeros((*rows, D // 16), device=device, dtype=torch.uint8)
+        self.slot_frame = torch.full((c.batch, c.window_frames), -1, device=device,
+                                     dtype=torch.int32)
+
+    def read(self, stream=None) -> torch.Tensor:
+        """The ring's values [B, W*tpf, D], as a Ring's cache holds them."""
+        out = torch.empty((*self.codes.shape[:2], self.c.d_c + self.c.d_rope),
+                          device=self.codes.device, dtype=api.torch_dtype(self.c))
+        api.mla_cache_read_q4(self.c, self.codes, self.scales, out, stream=stream)
+        return out
+
+    def state_dict(self):
+        return {"codes": self.codes.clone(), "scales": self.scales.clone(),
+                "slot_frame": self.slot_frame.clone()}
+
+    def load_state_dict(self, sd):
+        self.codes.copy_(sd["codes"])
+        self.scales.copy_(sd["scales"])
+        self.slot_frame.copy_(sd["slot_frame"])
+
+
+class ChunkBuffers:
+    """Per-chunk activations and scratch, allocated once per workload; q4: the scratch also serves
+    attention over a RingQ4."""
+
+    def __init__(self, c, device="cuda", fuse_uv: bool = True, q4: bool = False):
         tpf = c.frame_h * c.frame_w
         n_q = c.chunk_frames * tpf
         D = c.d_c + c.d_rope
@@ -88,7 +122,8 @@ class ChunkBuffers:
         self.o = torch.empty((B, n_q, H * c.d_head), device=device, dtype=dt)
         self.o_lat = torch.empty((B, n_q, H, c.d_c), device=device, dtype=dt)
         self.lse = torch.empty((B, H, n_q), device=device, dtype=torch.float32)
-        ws = api.mla_attention_workspace_bytes(c, c.window_frames)
+        ws = (api.mla_attention_q4_workspace_bytes if q4
+              else api.mla_attention_workspace_bytes)(c, c.window_frames)
         self.workspace = torch.empty((max(ws, 256),), device=device, dtype=torch.uint8)
         self.dev_status = torch.zeros((1,), device=device, dtype=torch.int32)
 
@@ -115,6 +150,10 @@ def attend_chunk(c, w: DeviceWeights, ring: Ring, buf: ChunkBuffers, chunk: int,
     fused form wherever the configuration allows it."""
     first, n_valid = chunk_schedule(c.chunk_frames, c.window_frames, chunk)
     out = buf.o if fuse_uv else buf.o_lat
+    if isinstance(ring, RingQ4):
+        _attend_q4(c, w, ring, buf, buf.x, n_valid, first, out, fuse_uv, _use_fused_q(c, fused_q),
+                   stream=stream)
+        return out
     if _use_fused_q(c, fused_q):
         _attend_from_cq(c, w, ring, buf, buf.x, n_valid, first, out, fuse_uv, buf.workspace,
                         rotate_ring=True, stream=stream)
@@ -143,9 +182,29 @@ def _attend_from_cq(c, w: DeviceWeights, ring: Ring, buf: ChunkBuffers, x, n_val
                                   prerotated=True)
 
 
+def _attend_q4(c, w: DeviceWeights, ring: RingQ4, buf: ChunkBuffers, x, n_valid: int, first: int,
+               out, fuse_uv: bool, fused_q: bool, stream=None) -> None:
+    """A chunk's projections and its attention over a ring held in 4 bits (the attention call
+    decodes the ring and writes every rotated key itself)."""
+    w_uv = w.w_uv if fuse_uv else None
+    state = (buf.chunk_lat, ring.codes, ring.scales, ring.slot_frame, n_valid, first, w_uv, out,
+             buf.lse, buf.workspace, buf.dev_status)
+    if fused_q:
+        api.mla_project_latents(c, x, w.w_x, buf.c_q, buf.chunk_lat, stream=stream)
+        api.mla_attention_fwd_from_cq_q4(c, buf.c_q, w.w_qcat, *state, stream=stream)
+    else:
+        api.mla_project_chunk(c, x, w.w_x, w.w_qcat, buf.c_q, buf.q, buf.chunk_lat, first,
+                              stream=stream)
+        api.mla_attention_fwd_q4(c, buf.q, *state, stream=stream)
+
+
 def append_chunk(c, ring: Ring, buf: ChunkBuffers, chunk: int, stream=None) -> None:
     """Moves the chunk's latents (buf.chunk_lat) into the ring, after its attention."""
     first, _ = chunk_schedule(c.chunk_frames, c.window_frames, chunk)
+    if isinstance(ring, RingQ4):
+        api.mla_cache_append_q4(c, buf.chunk_lat, ring.codes, ring.scales, ring.slot_frame, first,
+                                stream=stream)
+        return
     api.mla_cache_append(c, None, None, buf.chunk_lat, ring.cache, ring.slot_frame, first,
                          MLA_APPEND, stream=stream)
 
@@ -154,6 +213,11 @@ def prefill_chunk(c, w: DeviceWeights, ring: Ring, buf: ChunkBuffers, chunk: int
                   stream=None) -> None:
     """Projects buf.x and appends it to the ring without attending (cache warm-up)."""
     first, _ = chunk_schedule(c.chunk_frames, c.window_frames, chunk)
+    if isinstance(ring, RingQ4):
+        api.mla_cache_append(c, buf.x, w.w_dkv_kr, buf.chunk_lat, None, None, first, MLA_PROJECT,
+                             stream=stream)
+        append_chunk(c, ring, buf, chunk, stream=stream)
+        return
     api.mla_cache_append(c, buf.x, w.w_dkv_kr, buf.chunk_lat, ring.cache, ring.slot_frame, first,
                          MLA_PROJECT_AND_APPEND, stream=stream)
 
@@ -189,7 +253,8 @@ class HostStreamer:
 
     def __init__(self, c, w: DeviceWeights, ring: Ring, device="cuda", compute_stream=None):
         self.c, self.w, self.ring = c, w, ring
-        self.bufs = [ChunkBuffers(c, device=device), ChunkBuffers(c, device=device)]
+        q4 = isinstance(ring, RingQ4)
+        self.bufs = [ChunkBuffers(c, device=device, q4=q4) for _ in range(2)]
         self.compute = compute_stream or torch.cuda.current_stream(device)
         self.h2d = torch.cuda.Stream(device=device)
         self.d2h = torch.cuda.Stream(device=device)
@@ -274,7 +339,10 @@ class ChunkGraph:
         with torch.cuda.graph(self.graph, stream=side, capture_error_mode="relaxed"):
             if events:
                 self.proj_start.record()
-            if fused_q:
+            q4 = isinstance(ring, RingQ4)
+            if q4 and fused_q:
+                api.mla_project_latents(c, x, w.w_x, buf.c_q, buf.chunk_lat)
+            elif fused_q:
                 api.mla_project_latents_rotated(c, x, w.w_x, buf.c_q, buf.chunk_lat, ring.cache,
                                                 ring.slot_frame, n_valid, first, buf.workspace,
                                                 dev_status=buf.dev_status)
@@ -283,7 +351,14 @@ class ChunkGraph:
             if events:
                 self.attn_start.record()
             out = buf.o if fuse_uv else buf.o_lat
-            if fused_q:
+            if q4:
+                state = (buf.chunk_lat, ring.codes, ring.scales, ring.slot_frame, n_valid, first,
+                         w.w_uv if fuse_uv else None, out, buf.lse, buf.workspace, buf.dev_status)
+                if fused_q:
+                    api.mla_attention_fwd_from_cq_q4(c, buf.c_q, w.w_qcat, *state)
+                else:
+                    api.mla_attention_fwd_q4(c, buf.q, *state)
+            elif fused_q:
                 api.mla_attention_fwd_from_cq(c, buf.c_q, w.w_qcat, buf.chunk_lat, ring.cache,
                                               ring.slot_frame, n_valid, first,
                                               w.w_uv if fuse_uv else None, out, buf.lse,
@@ -294,8 +369,7 @@ class ChunkGraph:
                                       buf.workspace, buf.dev_status)
             if events:
                 self.attn_end.record()
-            api.mla_cache_append(c, None, None, buf.chunk_lat, ring.cache, ring.slot_frame,
-                                 first, MLA_APPEND)
+            append_chunk(c, ring, buf, chunk)
             if events:
                 self.append_end.record()
         torch.cuda.current_stream().wait_stream(side)
@@ -331,18 +405,23 @@ class LayerStack:
     One set of chunk activations (buf) is shared by all layers: a call's outputs are valid until
     the next call.  capture_chunk() records a whole chunk (rotations, every step and layer,
     appends) as one CUDA graph, with the step/layer inputs bound at capture time.
+
+    q4=True holds every layer's ring in 4 bits.  A layer then keeps no rotated keys of its own:
+    each call decodes and rotates what it attends to into one workspace that all layers share.
     """
 
     def __init__(self, c, weights, device="cuda", fuse_uv: bool = True,
-                 fused_q: Optional[bool] = None):
+                 fused_q: Optional[bool] = None, q4: bool = False):
         self.c = c
         # the query heads formed inside the attention kernel where the configuration allows
         self.fused_q = fused_query_supported(c) if fused_q is None else fused_q
         self.w = list(weights)
-        self.rings = [Ring(c, device=device) for _ in self.w]
+        self.q4 = q4
+        self.rings = [(RingQ4 if q4 else Ring)(c, device=device) for _ in self.w]
         ws = max(api.mla_attention_workspace_bytes(c, c.window_frames), 256)
-        self.ws = [torch.empty((ws,), device=device, dtype=torch.uint8) for _ in self.w]
-        self.buf = ChunkBuffers(c, device=device)
+        self.ws = [] if q4 else [torch.empty((ws,), device=device, dtype=torch.uint8)
+                                 for _ in self.w]
+        self.buf = ChunkBuffers(c, device=device, q4=q4)
         self.fuse_uv = fuse_uv
 
     @property
@@ -351,6 +430,8 @@ class LayerStack:
 
     def begin_chunk(self, chunk: int, stream=None) -> None:
         """Rotates every layer's ring keys for this chunk's (frozen) ring state."""
+        if self.q4:
+            return
         _, n_valid = chunk_schedule(self.c.chunk_frames, self.c.window_frames, chunk)
         for l in range(self.n_layers):
             api.mla_rotate_ring_keys(self.c, self.rings[l].cache, self.rings[l].slot_frame,
@@ -364,7 +445,10 @@ class LayerStack:
         c, b, w, ring = self.c, self.buf, self.w[layer], self.rings[layer]
         first, n_valid = chunk_schedule(c.chunk_frames, c.window_frames, chunk)
         out = b.o if self.fuse_uv else b.o_lat
-        if self.fused_q:
+        if self.q4:
+            _attend_q4(c, w, ring, b, x, n_valid, first, out, self.fuse_uv, self.fused_q,
+                       stream=stream)
+        elif self.fused_q:
             # the ring part of the layer's workspace was rotated by begin_chunk; the projection
             # writes the chunk's rotated keys next to it
             _attend_from_cq(c, w, ring, b, x, n_valid, first, out, self.fuse_uv, self.ws[layer],
@@ -377,8 +461,7 @@ class LayerStack:
                                               out, b.lse, self.ws[layer], b.dev_status,
                                               stream=stream)
         if append:
-            api.mla_cache_append(c, None, None, b.chunk_lat, ring.cache, ring.slot_frame, first,
-                                 MLA_APPEND, stream=stream)
+            append_chunk(c, ring, b, chunk, stream=stream)
         return out
 
     def run_chunk(self, chunk: int, n_steps: int, x_of, stream=None) -> None:
@@ -398,3 +481,41 @@ class LayerStack:
             self.run_chunk(chunk, n_steps, x_of)
         torch.cuda.current_stream().wait_stream(side)
         return g
+
+
+class EncoderStates:
+    """One layer's keys and values of an encoder's states (a prompt), projected once and attended
+    by every chunk and denoising step: k, v [B, n_kv, H_kv, d_head] and the number of valid states
+    per sample, kv_len [B] (None: all).  attend() is the layer's cross attention, backward() its
+    gradients; the backward's workspace is allocated by the first backward call, so backward calls
+    of one object are ordered on one stream."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, n_heads: int,
+                 kv_len: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None):
+        self.k, self.v, self.kv_len = k, v, kv_len
+        self.n_heads, self.softmax_scale = n_heads, softmax_scale
+        self.dev_status = torch.zeros((1,), device=k.device, dtype=torch.int32)
+        self.workspace = None
+
+    def config(self, n_q: int):
+        B, n_kv, n_kv_heads, d_head = self.k.shape
+        return api.make_cross_config(
+            batch=B, n_heads=self.n_heads, n_kv_heads=n_kv_heads, d_head=d_head, n_q=n_q,
+            n_kv=n_kv, softmax_scale=self.softmax_scale,
+            dtype="fp32" if self.k.dtype == torch.float32 else "bf16")
+
+    def attend(self, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+        """out [B, n_q, H, d_head] of the chunk's cross queries q; lse as the backward needs it."""
+        api.mla_cross_attention_fwd(self.config(q.shape[1]), q, self.k, self.v, out, lse=lse,
+                                    kv_len=self.kv_len, dev_status=self.dev_status, stream=stream)
+        return out
+
+    def backward(self, q, out, lse, d_out, d_q, d_k, d_v, stream=None) -> None:
+        cc = self.config(q.shape[1])
+        need = api.mla_cross_attention_bwd_workspace_bytes(cc)
+        if self.workspace is None or self.workspace.numel() < need:
+            self.workspace = torch.empty((need,), device=q.device, dtype=torch.uint8)
+        api.mla_cross_attention_bwd(cc, q, self.k, self.v, out, lse, d_out, d_q, d_k, d_v,
+                                    self.workspace, kv_len=self.kv_len,
+                                    dev_status=self.dev_status, stream=stream)

@@ -5,3 +5,4 @@ Only the tests, ``__graft_entry__.smoke()`` and the ``cpu_baseline`` /
 product path never calls it, and it shares no code with the CUDA library.
 """
 from .mla_oracle import *  # noqa: F401,F403
+from .cross_oracle import *  # noqa: F401,F403

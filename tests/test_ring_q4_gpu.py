@@ -1,0 +1,269 @@
+"""The latent ring held in 4 bits on the GPU: codes, scales and values bit for bit against the
+definition; attention over it bit for bit against the same call on the ring's values, and those
+values' rollout against the float64 oracle."""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from mla_latent_kv_attn_b200 import api, inputs, rollout
+from parity_util import GpuRun, OracleRun, check_chunk, to_np
+
+pytestmark = pytest.mark.gpu
+
+SMALL = inputs.small_bf16_config()
+TOY16 = inputs.with_latent_shape(inputs.CONFIGS[0], 16, 16)      # fp32, whole groups
+PATHS = {"tc": api.MLA_PATH_AUTO, "pair": api.MLA_PATH_TC_PAIR, "simt": api.MLA_PATH_SIMT}
+
+
+def _chunk(c, seed, std=1.0):
+    n_q = c.chunk_frames * c.frame_h * c.frame_w
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((c.batch, n_q, c.d_c + c.d_rope), generator=g, device="cuda") * std
+    return x.to(api.torch_dtype(c))
+
+
+def _append(c, ring, lat, first):
+    api.mla_cache_append_q4(c, lat, ring.codes, ring.scales, ring.slot_frame, first)
+
+
+def _edge_values(lat):
+    """Rows with what a group can hold at its edges."""
+    x = lat.clone()
+    x[0, 0] = 0
+    x[0, 1, :16] = 1.75                       # max / 7 is a scale itself
+    x[0, 2, :16] = 1e-8                       # below the smallest scale
+    x[0, 3, 5] = 1e6                          # beyond the largest: saturates
+    x[0, 4, :16] = torch.arange(-8, 8, device="cuda") / 2 * 0.25   # ties between codes
+    x[0, 5, 3] = float("nan")
+    x[0, 6, 3] = float("inf")
+    x[0, 7, 3] = -float("inf")
+    x[0, 8] = -0.0
+    return x
+
+
+@pytest.mark.parametrize("cfg", [SMALL, TOY16, inputs.with_latent_shape(SMALL, 256, 64),
+                                 dataclasses.replace(SMALL, frame_h=3, frame_w=7, window_frames=5,
+                                                     chunk_frames=2, batch=3)],
+                         ids=["small", "fp32", "wide", "odd"])
+def test_append_and_read_match_the_definition(cfg):
+    c = api.make_config(cfg)
+    tpf, W, D = cfg.tokens_per_frame, cfg.window_frames, cfg.d_latent
+    ring = rollout.RingQ4(c)
+    assert (ring.read() == 0).all()
+    codes = np.full((cfg.batch, W, tpf, D // 2), 0x88, np.uint8)
+    scales = np.zeros((cfg.batch, W, tpf, D // 16), np.uint8)
+    slots = np.full((cfg.batch, W), -1, np.int32)
+    for ch in range(4):                                    # wraps
+        lat = _edge_values(_chunk(c, ch, std=10.0 ** (ch - 2)))
+        first = ch * cfg.chunk_frames
+        _append(c, ring, lat, first)
+        # a NaN is stored as 0 and passed over by the group's maximum
+        x = np.nan_to_num(to_np(lat), nan=0.0, posinf=1e30, neginf=-1e30)
+        qc, qs = oracle.q4_encode(x)
+        for f in range(cfg.chunk_frames):
+            s = (first + f) % W
+            codes[:, s], scales[:, s] = qc[:, f * tpf:(f + 1) * tpf], qs[:, f * tpf:(f + 1) * tpf]
+            slots[:, s] = first + f
+        assert np.array_equal(ring.codes.cpu().numpy().reshape(codes.shape), codes), ch
+        assert np.array_equal(ring.scales.cpu().numpy().reshape(scales.shape), scales), ch
+        assert np.array_equal(ring.slot_frame.cpu().numpy(), slots), ch
+        assert np.array_equal(to_np(ring.read()).reshape(cfg.batch, W, tpf, D),
+                              oracle.q4_decode(codes, scales)), ch
+
+
+def _filled(cfg, path, chunks, seed=0):
+    """A 4-bit ring after `chunks` appends, and a plain ring holding its values."""
+    c = api.make_config(cfg, kernel_path=path)
+    q4, plain = rollout.RingQ4(c), rollout.Ring(c)
+    for ch in range(chunks):
+        _append(c, q4, _chunk(c, seed + ch), ch * cfg.chunk_frames)
+    plain.cache.copy_(q4.read())
+    plain.slot_frame.copy_(q4.slot_frame)
+    return c, q4, plain
+
+
+def _query(c, seed):
+    n_q = c.chunk_frames * c.frame_h * c.frame_w
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randn((c.batch, n_q, c.n_heads, c.d_c + c.d_rope), generator=g, device="cuda")
+    w_uv = torch.randn((c.n_heads, c.d_head, c.d_c), generator=g, device="cuda") * c.d_c ** -0.5
+    return q.to(api.torch_dtype(c)), w_uv.to(api.torch_dtype(c))
+
+
+@pytest.mark.parametrize("chunks", [0, 1, 5])
+@pytest.mark.parametrize("fuse_uv", [True, False])
+@pytest.mark.parametrize("path,d_c,d_rope", [("tc", 192, 32), ("tc", 128, 16), ("tc", 256, 64),
+                                             ("pair", 192, 32), ("simt", 192, 32)])
+def test_attention_equals_the_call_on_the_rings_values(path, d_c, d_rope, fuse_uv, chunks):
+    cfg = inputs.with_latent_shape(SMALL, d_c, d_rope)
+    c, q4, plain = _filled(cfg, PATHS[path], chunks)
+    first, n_valid = rollout.chunk_schedule(cfg.chunk_frames, cfg.window_frames, chunks)
+    lat, (q, w_uv) = _chunk(c, 100), _query(c, 101)
+    a, b = rollout.ChunkBuffers(c), rollout.ChunkBuffers(c, q4=True)
+    b.workspace.fill_(0xFF)                                # contents on entry must not matter
+    outs = []
+    for buf in (a, b):
+        out = buf.o if fuse_uv else buf.o_lat
+        w = w_uv if fuse_uv else None
+        if buf is a:
+            api.mla_attention_fwd(c, q, lat, plain.cache, plain.slot_frame, n_valid, first, w, out,
+                                  buf.lse, buf.workspace, buf.dev_status)
+        else:
+            need = max(api.mla_attention_q4_workspace_bytes(c, n_valid), 256)
+            api.mla_attention_fwd_q4(c, q, lat, q4.codes, q4.scales, q4.slot_frame, n_valid, first,
+                                     w, out, buf.lse, buf.workspace[:need], buf.dev_status)
+            assert (buf.workspace[need:] == 0xFF).all()
+        outs.append((out, buf.lse))
+    torch.cuda.synchronize()
+    rollout.check_device_status(b)
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("chunks", [0, 2, 5])
+@pytest.mark.parametrize("d_c,d_rope", [(192, 32), (128, 64)])
+def test_attention_from_cq_equals_the_call_on_the_rings_values(d_c, d_rope, chunks):
+    cfg = inputs.with_latent_shape(SMALL, d_c, d_rope)
+    c, q4, plain = _filled(cfg, api.MLA_PATH_AUTO, chunks)
+    first, n_valid = rollout.chunk_schedule(cfg.chunk_frames, cfg.window_frames, chunks)
+    lat, (_, w_uv) = _chunk(c, 100), _query(c, 101)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    c_q = torch.randn((cfg.batch, cfg.n_q, c.d_cq), generator=g, device="cuda").bfloat16()
+    w_q = (torch.randn((c.n_heads, cfg.d_latent, c.d_cq), generator=g, device="cuda")
+           * c.d_cq ** -0.5).bfloat16()
+    a, b = rollout.ChunkBuffers(c), rollout.ChunkBuffers(c, q4=True)
+    api.mla_attention_fwd_from_cq(c, c_q, w_q, lat, plain.cache, plain.slot_frame, n_valid, first,
+                                  w_uv, a.o, a.lse, a.workspace, a.dev_status)
+    api.mla_attention_fwd_from_cq_q4(c, c_q, w_q, lat, q4.codes, q4.scales, q4.slot_frame, n_valid,
+                                     first, w_uv, b.o, b.lse, b.workspace, b.dev_status)
+    torch.cuda.synchronize()
+    rollout.check_device_status(b)
+    assert torch.equal(a.o, b.o) and torch.equal(a.lse, b.lse)
+
+
+def test_fp32_ring_on_cuda_cores():
+    c, q4, plain = _filled(TOY16, api.MLA_PATH_AUTO, 3)
+    first, n_valid = rollout.chunk_schedule(TOY16.chunk_frames, TOY16.window_frames, 3)
+    lat, (q, w_uv) = _chunk(c, 100), _query(c, 101)
+    a, b = rollout.ChunkBuffers(c), rollout.ChunkBuffers(c, q4=True)
+    api.mla_attention_fwd(c, q, lat, plain.cache, plain.slot_frame, n_valid, first, w_uv, a.o,
+                          a.lse, a.workspace, a.dev_status)
+    api.mla_attention_fwd_q4(c, q, lat, q4.codes, q4.scales, q4.slot_frame, n_valid, first, w_uv,
+                             b.o, b.lse, b.workspace, b.dev_status)
+    assert torch.equal(a.o, b.o) and torch.equal(a.lse, b.lse)
+
+
+@pytest.mark.parametrize("fused_q", [True, False])
+def test_rollout_matches_the_oracle_on_the_quantised_ring(fused_q):
+    """A rollout whose ring wraps, with cross attention to a prompt between the chunks: every
+    chunk's output against the oracle whose window holds the 4-bit ring's own values."""
+    cfg = SMALL
+    g, o = GpuRun(cfg), OracleRun(cfg, inputs.layer_weights(cfg))
+    g.ring, g.buf = rollout.RingQ4(g.c), rollout.ChunkBuffers(g.c, q4=True)
+    rows = np.arange(cfg.n_q)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    kv = torch.randn((2, cfg.batch, 50, cfg.n_heads, cfg.d_head), generator=gen, device="cuda")
+    text = rollout.EncoderStates(kv[0].bfloat16(), kv[1].bfloat16(), n_heads=cfg.n_heads,
+                                 kv_len=torch.tensor([50, 21], device="cuda", dtype=torch.int32))
+    for ch in range(cfg.n_chunks):
+        x = inputs.chunk_x(cfg, ch)
+        g.load_x(x)
+        out = rollout.attend_chunk(g.c, g.w, g.ring, g.buf, ch, fused_q=fused_q)
+        q = out.unflatten(-1, (cfg.n_heads, cfg.d_head))
+        cross = text.attend(q, torch.empty_like(q))
+        rollout.append_chunk(g.c, g.ring, g.buf, ch)
+        torch.cuda.synchronize()
+        rollout.check_device_status(g.buf)
+        ores = o.step(ch, x, rows)
+        check_chunk(f"q4.chunk{ch}", cfg, dict(o=to_np(out), lse=to_np(g.buf.lse),
+                                               c_q=to_np(g.buf.c_q),
+                                               chunk_lat=to_np(g.buf.chunk_lat)), ores, rows)
+        want, _, e, _ = oracle.cross_attention(to_np(q), to_np(text.k), to_np(text.v), [50, 21],
+                                               cfg.d_head ** -0.5, p_rel=2.0 ** -8 + 1.1e-4)
+        assert (np.abs(to_np(cross) - want) <= e * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want)).all()
+        # the oracle's window takes the values that the ring stands for
+        values = to_np(g.ring.read())
+        tpf = cfg.tokens_per_frame
+        for b in range(cfg.batch):
+            for rec in o.windows[b].frames:
+                s = rec.t % cfg.window_frames
+                v = values[b, s * tpf:(s + 1) * tpf]
+                rec.c_kv, rec.k_r = v[:, :cfg.d_c], v[:, cfg.d_c:]
+    assert int(text.dev_status) == 0
+
+
+def test_layer_stack_and_graphs_over_4_bit_rings():
+    """Layers that share one workspace, eager and captured, and a chunk graph: the same bits."""
+    cfg = SMALL
+    c = api.make_config(cfg)
+    lws = [inputs.layer_weights(cfg, l) for l in range(2)]
+    xs = {(ch, s, l): torch.from_numpy(inputs.chunk_x(cfg, ch, s, l)).to(torch.bfloat16).cuda()
+          for ch in range(cfg.n_chunks) for s in range(2) for l in range(2)}
+    eager = rollout.LayerStack(c, [rollout.upload_weights(c, lw) for lw in lws], q4=True)
+    graphed = rollout.LayerStack(c, [rollout.upload_weights(c, lw) for lw in lws], q4=True)
+    for ch in range(cfg.n_chunks):
+        x_of = lambda s, l, ch=ch: xs[(ch, s, l)]
+        eager.run_chunk(ch, 2, x_of)
+        want = eager.buf.o.clone()
+        graphed.capture_chunk(ch, 2, x_of).replay()
+        torch.cuda.synchronize()
+        assert torch.equal(graphed.buf.o, want), ch
+        for a, b in zip(eager.rings, graphed.rings):
+            assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+            assert torch.equal(a.slot_frame, b.slot_frame)
+    rollout.check_device_status(graphed.buf)
+    # the same rollout of layer 0 by hand and by chunk graphs
+    w = rollout.upload_weights(c, lws[0])
+    one, two = rollout.RingQ4(c), rollout.RingQ4(c)
+    b1, b2 = rollout.ChunkBuffers(c, q4=True), rollout.ChunkBuffers(c, q4=True)
+    for ch in range(cfg.n_chunks):
+        b1.x.copy_(xs[(ch, 1, 0)])
+        o1 = rollout.run_chunk(c, w, one, b1, ch)
+        o2 = rollout.ChunkGraph(c, w, two, b2, ch, x=xs[(ch, 1, 0)]).replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o1, o2)
+    assert torch.equal(one.codes, two.codes) and torch.equal(one.codes, eager.rings[0].codes)
+    saved = one.state_dict()
+    three = rollout.RingQ4(c)
+    three.load_state_dict(saved)
+    assert torch.equal(three.read(), one.read())
+
+
+def test_streamer_prefill_and_side_stream():
+    cfg = SMALL
+    c = api.make_config(cfg)
+    w = rollout.upload_weights(c, inputs.layer_weights(cfg))
+    a, b = rollout.RingQ4(c), rollout.RingQ4(c)
+    buf, other = rollout.ChunkBuffers(c, q4=True), rollout.ChunkBuffers(c, q4=True)
+    side = torch.cuda.Stream()
+    x = torch.from_numpy(inputs.chunk_x(cfg, 0)).to(torch.bfloat16).cuda()
+    buf.x.copy_(x)
+    other.x.copy_(x)
+    rollout.run_chunk(c, w, a, buf, 0)
+    side.wait_stream(torch.cuda.current_stream())
+    rollout.prefill_chunk(c, w, b, other, 0, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+
+
+def test_bad_calls_are_refused():
+    c, q4, _ = _filled(SMALL, api.MLA_PATH_AUTO, 1)
+    buf = rollout.ChunkBuffers(c, q4=True)
+    lat, (q, w_uv) = _chunk(c, 0), _query(c, 1)
+    call = lambda ws=buf.workspace, codes=q4.codes, n_valid=3: api.mla_attention_fwd_q4(
+        c, q, lat, codes, q4.scales, q4.slot_frame, n_valid, 3, w_uv, buf.o, buf.lse, ws,
+        buf.dev_status)
+    call()
+    need = api.mla_attention_q4_workspace_bytes(c, 3)
+    for bad in (dict(ws=buf.workspace[:need - 1]), dict(ws=None), dict(ws=buf.workspace[16:]),
+                dict(n_valid=c.window_frames + 1), dict(codes=q4.codes.cpu())):
+        with pytest.raises(api.MLAError):
+            call(**bad)
+    with pytest.raises(ValueError):
+        call(codes=q4.codes[:, :-1])
+    # a workspace sized for a plain ring does not serve
+    with pytest.raises(api.MLAError):
+        call(ws=rollout.ChunkBuffers(c).workspace)
