@@ -57,4 +57,8 @@ mla_status cross_bwd_simt(const CrossDims& d, const CrossBwdArgs& a, float* delt
 mla_status cross_delta(const CrossDims& d, const void* out, const void* d_out, float* delta,
                        cudaStream_t s);
 
+// Tensor-core kernels: bf16 with d 64 or 128 (cross_sm100.cu).
+bool cross_tc_supported(const CrossDims& d);
+mla_status cross_fwd_tc(const CrossDims& d, const CrossArgs& a, cudaStream_t s);
+
 }  // namespace mla

@@ -909,7 +909,8 @@ mla_status mla_cross_attention_fwd(const mla_cross_config* cfg, const void* q, i
   MLA_TRY(check_ptr(dev_status, "dev_status", false));
   CrossArgs a{};
   a.q = q; a.k = k; a.v = v; a.kv_len = kv_len; a.out = out; a.lse = lse; a.dev_status = dev_status;
-  return cross_fwd_simt(d, a, static_cast<cudaStream_t>(stream));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cross_tc_supported(d) ? cross_fwd_tc(d, a, s) : cross_fwd_simt(d, a, s);
 }
 
 size_t mla_cross_attention_bwd_workspace_bytes(const mla_cross_config* cfg) {
