@@ -5,19 +5,27 @@
 // streams of 128 rows that share every key and value tile: while one stream's softmax runs on the
 // CUDA cores, the other's products run on the tensor cores.  (With 128 rows per item the keys and
 // values would cross L2 -> SM twice as often, 114 MB in the call of 4680 queries, 12 heads and 512
-// states, whose products take 9 us.)  Roles (352 threads):
-//   warps 0-3, 4-7  softmax of stream 0, 1: one TMEM lane (query row) per thread; online softmax in
-//                   the log2 domain, O rescaled only when a row's maximum grows by more than 2^8;
-//                   P rounded to bf16 (the tensor cores' operand type; the row sum l is taken from
-//                   the unrounded values in fp32); O / l, lse
-//   warp 8          TMA producer: the item's two Q tiles, then K_0, V_0, K_1, V_1, ... (128 states
-//                   each) through a ring of shared-memory stages
-//   warps 9, 10     MMA issuer of stream 0, 1: S = Q K_j^T (both in shared memory) and
-//                   O += P_j V_j (P in TMEM, V read MN-major)
-// TMEM, 512 columns: two S buffers, two O accumulators and, for d 64, two P buffers.  For d 128
-// nothing is left for P: it takes the second half of its S buffer, and QK(j+1) waits for PV(j).
-// P becomes visible to PV in two halves of 64 states, so PV starts while the second half of the
-// exponentials is still being computed.
+// states, whose products take 9 us.)  Roles (640 threads):
+//   warps 0-15    softmax; stream = warp / 8, and within a stream two warps share 32 TMEM lanes
+//                 (query rows), each with half of a tile's states.  Online softmax in the log2
+//                 domain, the halves' maxima exchanged through shared memory, O rescaled only when
+//                 a row's maximum grows by more than 2^8; P rounded to bf16 (the tensor cores'
+//                 operand type; the row sum l is taken from the unrounded values in fp32); O / l
+//                 into shared memory, lse
+//   warp 16       TMA producer: the item's two Q tiles (into the buffer that the item before last
+//                 left), then K_0, V_0, K_1, V_1, ... (128 states each) through a ring of stages
+//   warps 17, 18  MMA issuer of stream 0, 1: S = Q K_j^T (both in shared memory) and
+//                 O += P_j V_j (P in TMEM, V read MN-major)
+//   warp 19       TMA stores of O from the item's Q buffer.  (Stored by the softmax threads, 16
+//                 bytes of 32 rows at a time, O took 9000 cycles an item.)
+// TMEM, 512 columns: two S buffers, two O accumulators and, for d 64, two P buffers; QK(j+1) then
+// runs under the softmax of j.  For d 128 nothing is left for P and it takes the place of S: each
+// half of the states' 64 columns become 32 columns of bf16 pairs (written by the threads that read
+// them), and QK(j+1) waits for PV(j).  A thread holds 32 scores at a time and reads S up to twice: with 64
+// in registers (96 a thread) the spills went past the little L1 that the tiles leave, and a tile's
+// softmax took 4000 cycles.
+// An item's first QK of stream 1 waits for that of stream 0: streams in step would load the tensor
+// and the CUDA cores in turn (6000 cycles a pair of tiles, against 2048 of products and 4500 as it is).
 // States past a sample's length are masked: their scores become -infinity by selection, and their
 // value rows are overwritten with zeros in shared memory (0 * NaN would reach O).
 #include "cross.h"
@@ -33,9 +41,11 @@ using namespace sm100;
 
 constexpr int kBM = 128;             // query rows of a stream
 constexpr int kBN = 128;             // states of a tile
-constexpr int kProducerWarp = 8;
-constexpr int kIssuerWarp = 9;       // and 10; warp 9 also allocates TMEM
-constexpr int kThreads = 352;
+constexpr int kStreamThreads = 256;
+constexpr int kProducerWarp = 16;
+constexpr int kIssuerWarp = 17;      // and 18; warp 17 also allocates TMEM
+constexpr int kStoreWarp = 19;
+constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -47,14 +57,17 @@ struct FwdShape {
   static constexpr int kBlocks = D / 64;                  // 64-column blocks, 128B swizzle
   static constexpr int kBlk = kBM * 128;                  // 16 KB
   static constexpr int kTile = kBlocks * kBlk;
-  static constexpr int kStages = D == 128 ? 5 : 8;
-  static constexpr int kSmem = (2 + kStages) * kTile + 1024;
-  static_assert(kSmem + 512 <= 227 * 1024, "shared memory");
-  static constexpr bool kAliasP = D == 128;
+  static constexpr int kStages = D == 128 ? 3 : 8;
+  static constexpr int kSmem = (4 + kStages) * kTile + 3072;      // tiles, then FwdShared
+  static_assert(kSmem <= 227 * 1024, "shared memory");
   // Pairs (out of every 8) whose exponentials take the FMA-pipe polynomial instead of the SFU.
   static constexpr int kPolyPairs = 2;
+  static constexpr bool kAliasP = D == 128;               // P in the columns of its S buffer
   static constexpr uint32_t s_col(int i) { return 128u * i; }
-  static constexpr uint32_t p_col(int i) { return kAliasP ? 128u * i + 64u : 256u + 64u * i; }
+  // 32 columns of P for half `ch` of the states
+  static constexpr uint32_t p_col(int i, int ch) {
+    return kAliasP ? s_col(i) + 64u * ch : 256u + 64u * i + 32u * ch;
+  }
   static constexpr uint32_t o_col(int i) { return kAliasP ? 256u + 128u * i : 384u + 64u * i; }
 };
 
@@ -67,6 +80,24 @@ struct CrossFwdParams {
   float* lse;
   int32_t* dev_status;
 };
+
+// Barriers and small data behind the tiles.
+template <int kStages>
+struct FwdShared {
+  uint64_t q_full[2][2], q_empty[2][2];     // [stream][buffer]
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[2];        // S(j) complete
+  uint64_t s_free[2];        // S(j) has been read (when P has its own columns)
+  uint64_t p_full[2][2];     // states 0-63, 64-127 of P(j) are in TMEM
+  uint64_t pv_done[2];       // PV(j) complete
+  uint64_t o_free[2];        // the item's O is in registers
+  uint64_t o_staged[2];      // and in the item's Q buffer
+  uint64_t first_qk[2];      // stream 0's first S of an item (by parity)
+  float part[2][2][kBM];     // [stream][half]: row maxima, row sums
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(FwdShared<8>) <= 3072, "shared memory");
 
 struct Item {
   int b, h, q0, len, nt;
@@ -83,18 +114,38 @@ __device__ __forceinline__ Item item_of(const CrossFwdParams& p, int it) {
   return w;
 }
 
-// Zeros rows [from, 128) of a tile of kBlocks blocks of 128-byte rows (whatever the swizzle: it
+// Zeros rows [from, to) of a tile of kBlocks blocks of 128-byte rows (whatever the swizzle: it
 // permutes within a row), `threads` threads of index t.
 template <int kBlocks>
-__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int t, int threads) {
-  const int n = (128 - from) * 8 * kBlocks;
+__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int to, int t, int threads) {
+  const int n = (to - from) * 8;
   for (int i = t; i < n; i += threads) {
-    const int blk = i / ((128 - from) * 8), o = i % ((128 - from) * 8);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + blk * 128 * 128 +
-                                                                  from * 128 + o * 16),
-                 "r"(0)
-                 : "memory");
+#pragma unroll
+    for (int blk = 0; blk < kBlocks; ++blk)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + blk * 128 * 128 +
+                                                                    from * 128 + i * 16),
+                   "r"(0)
+                   : "memory");
   }
+}
+
+// The largest of 32 scores; those from `valid` on become -infinity.
+__device__ __forceinline__ float masked_max(uint32_t (&s)[32], int valid) {
+  if (valid < 32) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (c >= valid) s[c] = 0xff800000u;
+  }
+  float m4[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float a = fmax3(__uint_as_float(s[k]), __uint_as_float(s[k + 4]), __uint_as_float(s[k + 8]));
+#pragma unroll
+    for (int c = 12; c < 28; c += 8)
+      a = fmax3(a, __uint_as_float(s[c + k]), __uint_as_float(s[c + 4 + k]));
+    m4[k] = fmaxf(a, __uint_as_float(s[28 + k]));
+  }
+  return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
 }
 
 // p = 2^(s scale - m) of kN consecutive scores of a row, packed to bf16 pairs; returns their sum.
@@ -126,36 +177,42 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, CrossFwdParams p) {
+                        const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_o, CrossFwdParams p) {
   using Sh = FwdShape<D>;
   constexpr int kStages = Sh::kStages, kTile = Sh::kTile, kBlk = Sh::kBlk;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t q_full[2], q_empty[2];
-  __shared__ __align__(8) uint64_t kv_full[kStages], kv_empty[kStages];
-  __shared__ __align__(8) uint64_t s_full[2];      // S(j) complete
-  __shared__ __align__(8) uint64_t s_free[2];      // S(j) is in registers (P in its own columns)
-  __shared__ __align__(8) uint64_t p_half[2][2];   // states 0-63, 64-127 of P(j) are in TMEM
-  __shared__ __align__(8) uint64_t pv_done[2];     // PV(j) complete
-  __shared__ __align__(8) uint64_t o_free[2];      // the item's O is in registers
-  __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_sh;
-
-  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sQ = sbase, sKV = sbase + 2 * kTile;
+  // (the declared alignment is the swizzle's; there is no shared memory beside this)
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t sQ = smem_u32(smem_raw), sKV = sQ + 4 * kTile;  // Q buffer b of stream i: 2 i + b
+  FwdShared<kStages>& sh = *reinterpret_cast<FwdShared<kStages>*>(smem_raw + (4 + kStages) * kTile);
+  auto& q_full = sh.q_full;
+  auto& q_empty = sh.q_empty;
+  auto& kv_full = sh.kv_full;
+  auto& kv_empty = sh.kv_empty;
+  auto& s_full = sh.s_full;
+  auto& s_free = sh.s_free;
+  auto& p_full = sh.p_full;
+  auto& pv_done = sh.pv_done;
+  auto& o_free = sh.o_free;
+  auto& o_staged = sh.o_staged;
+  auto& first_qk = sh.first_qk;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  volatile int* abort_flag = &abort_sh;
+  volatile int* abort_flag = &sh.abort_flag;
 
   if (threadIdx.x == 0) {
-    abort_sh = 0;
+    sh.abort_flag = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&q_full[i]), 1);
-      mbar_init(smem_u32(&q_empty[i]), 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_u32(&q_full[i][b]), 1);
+        mbar_init(smem_u32(&q_empty[i][b]), 1);
+        mbar_init(smem_u32(&p_full[i][b]), kBM);
+      }
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&s_free[i]), kBM);
-      mbar_init(smem_u32(&p_half[i][0]), kBM);
-      mbar_init(smem_u32(&p_half[i][1]), kBM);
+      mbar_init(smem_u32(&s_free[i]), kStreamThreads);
       mbar_init(smem_u32(&pv_done[i]), 1);
-      mbar_init(smem_u32(&o_free[i]), kBM);
+      mbar_init(smem_u32(&o_free[i]), kStreamThreads);
+      mbar_init(smem_u32(&o_staged[i]), kStreamThreads);
+      mbar_init(smem_u32(&first_qk[i]), 1);
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&kv_full[s]), 1);
@@ -164,13 +221,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   if (warp == kIssuerWarp) {
-    tmem_alloc(smem_u32(&tmem_base_sh), kTmemCols);
+    tmem_alloc(smem_u32(&sh.tmem_base), kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base_sh;
+  const uint32_t tmem = sh.tmem_base;
   grid_dep_wait();
   grid_dep_launch();
 
@@ -183,20 +240,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
-      uint32_t n_item[2] = {0, 0}, u = 0;          // uses of the Q tiles and of the ring
+      uint32_t n_item[2] = {0, 0}, u = 0;          // items of the streams, uses of the ring
       bool ok = true;
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
         const Item w = item_of(p, it);
         if (w.nt == 0) continue;
         for (int i = 0; i < 2 && ok; ++i) {
           if (w.q0 + i * kBM >= p.n_q) break;
-          ok = wait(q_empty[i], n_item[i] + 1);
+          const int b = n_item[i] & 1;
+          ok = wait(q_empty[i][b], (n_item[i] >> 1) + 1);
           if (!ok) break;
           ++n_item[i];
-          const uint32_t fb = smem_u32(&q_full[i]);
+          const uint32_t fb = smem_u32(&q_full[i][b]);
           mbar_arrive_expect_tx(fb, kTile);
           for (int k = 0; k < Sh::kBlocks; ++k)
-            tma_load_4d(sQ + i * kTile + k * kBlk, &tm_q, fb, 64 * k, w.h, w.q0 + i * kBM, w.b);
+            tma_load_4d(sQ + (2 * i + b) * kTile + k * kBlk, &tm_q, fb, 64 * k, w.h,
+                        w.q0 + i * kBM, w.b);
         }
         for (int j = 0; j < 2 * w.nt && ok; ++j, ++u) {
           const int s = u % kStages;
@@ -210,18 +269,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+  } else if (warp == kStoreWarp) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_o);
+      uint32_t n_item[2] = {0, 0};
+      bool ok = true;
+      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+        const Item w = item_of(p, it);
+        if (w.nt == 0) continue;
+        for (int i = 0; i < 2; ++i) {
+          if (w.q0 + i * kBM >= p.n_q) break;
+          ok = wait(o_staged[i], n_item[i]);
+          if (!ok) break;
+          const int b = n_item[i]++ & 1;
+          for (int k = 0; k < Sh::kBlocks; ++k)     // (rows past n_q are not written)
+            tma_store_4d(&tm_o, sQ + (2 * i + b) * kTile + k * kBlk, 64 * k, w.h, w.q0 + i * kBM,
+                         w.b);
+          bulk_commit_group();
+          bulk_wait_group_read<0>();
+          mbar_arrive(smem_u32(&q_empty[i][b]));
+        }
+      }
+      bulk_wait_group_all();
+    }
   } else if (warp >= kIssuerWarp) {
     const int i = warp - kIssuerWarp;
     if (lane == 0) {
       constexpr uint32_t idesc_qk = idesc_bf16_f32(kBM, kBN, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(kBM, D, 0, 1);
-      const uint64_t qd = smem_desc(sQ + i * kTile, 16, 1024, kSwizzle128B);
+      const uint64_t qd0 = smem_desc(sQ + 2 * i * kTile, 16, 1024, kSwizzle128B);
       const uint64_t kd0 = smem_desc(sKV, 16, 1024, kSwizzle128B);
       const uint64_t vd0 = smem_desc(sKV, kBlk, 1024, kSwizzle128B);
-      const uint32_t ts = tmem + Sh::s_col(i), tp = tmem + Sh::p_col(i), to = tmem + Sh::o_col(i);
+      const uint32_t ts = tmem + Sh::s_col(i), to = tmem + Sh::o_col(i);
       uint32_t n_item = 0, t = 0, u0 = 0;   // items and tiles of this stream, uses of the ring
+      uint32_t n_both = 0;                  // items in which both streams have rows
       bool ok = true;
       const auto issue_qk = [&](uint32_t u) {
+        const uint64_t qd = qd0 + ((n_item & 1) * kTile >> 4);
         const uint64_t kd = kd0 + ((u % kStages) * kTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -241,38 +325,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           continue;
         }
-        ok = wait(q_full[i], n_item);
+        const bool both = w.q0 + kBM < p.n_q;
+        ok = wait(q_full[i][n_item & 1], n_item >> 1);
+        // Stream 0 cannot be two such items ahead of stream 1 (whose Q buffers would have to be
+        // free again), so a barrier for each parity tells the items apart.
+        if (i == 1) ok = ok && wait(first_qk[n_both & 1], n_both >> 1);
         for (int j = 0; j < w.nt && ok; ++j) {
           const uint32_t uk = u0 + 2 * j, uv = uk + 1;
           if (Sh::kAliasP || j == 0) {
             // the S buffer: PV of the last tile has read P out of it, or (P in its own columns)
-            // the softmax has loaded that tile's S
+            // the softmax has read that tile's S
             ok = wait(kv_full[uk % kStages], uk / kStages) &&
                  (t == 0 || wait(Sh::kAliasP ? pv_done[i] : s_free[i], t - 1));
             if (!ok) break;
             tc_fence_after();
             issue_qk(uk);
-            if (j == w.nt - 1) mma_commit(smem_u32(&q_empty[i]));
+            if (i == 0 && j == 0 && both) mma_commit(smem_u32(&first_qk[n_both & 1]));
           }
-          if (!Sh::kAliasP && j + 1 < w.nt) {      // QK(j+1) runs under the softmax of j
+          if (!Sh::kAliasP && j + 1 < w.nt) {
             const uint32_t un = uk + 2;
             ok = wait(kv_full[un % kStages], un / kStages) && wait(s_free[i], t);
             if (!ok) break;
             tc_fence_after();
             issue_qk(un);
-            if (j + 1 == w.nt - 1) mma_commit(smem_u32(&q_empty[i]));
           }
           ok = wait(kv_full[uv % kStages], uv / kStages) &&
                (j > 0 || n_item == 0 || wait(o_free[i], n_item - 1));
           const uint64_t vd = vd0 + ((uv % kStages) * kTile >> 4);
           for (int half = 0; half < 2 && ok; ++half) {
-            ok = wait(p_half[i][half], t);
+            ok = wait(p_full[i][half], t);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int k4 = 0; k4 < 4; ++k4) {
               const int kk = 4 * half + k4;
-              mma_ts(to, tp + 8 * kk, vd + 128 * kk, idesc_pv, (j | kk) != 0 ? 1u : 0u);
+              mma_ts(to, tmem + Sh::p_col(i, half) + 8 * k4, vd + 128 * kk, idesc_pv, (j | kk) != 0 ? 1u : 0u);
             }
           }
           if (!ok) break;
@@ -282,29 +369,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         u0 += 2 * w.nt;
         ++n_item;
+        n_both += both;
       }
     }
   } else {
     // ------------------------------------------------------------------ softmax
-    const int i = warp / 4;                              // stream
+    const int i = warp / 8, ch = (warp / 4) & 1;         // stream, half of the states
     const int row = (warp % 4) * 32 + lane;              // TMEM lane
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-    const uint32_t ts = tl + Sh::s_col(i), tp = tl + Sh::p_col(i), to = tl + Sh::o_col(i);
+    const uint32_t ts = tl + Sh::s_col(i) + 64 * ch, tp = tl + Sh::p_col(i, ch);
+    const uint32_t to = tl + Sh::o_col(i) + D / 2 * ch;
+    float* mine = &sh.part[i][ch][row];
+    const float* other = &sh.part[i][ch ^ 1][row];
     const auto wait_all = [&](uint64_t& bar, uint32_t phase) {
       return __all_sync(0xffffffffu, wait(bar, phase)) != 0;
     };
-    uint32_t t = 0, u0 = 0;
+    uint32_t t = 0, u0 = 0, n_item = 0;
     bool ok = true;
     for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
       const Item w = item_of(p, it);
-      const int n = w.q0 + i * kBM + row;
-      const int64_t sr = (static_cast<int64_t>(w.b) * p.H + w.h) * p.n_q + n;
-      bf16* orow = p.out + ((static_cast<int64_t>(w.b) * p.n_q + n) * p.H + w.h) * D;
       if (w.nt == 0) {
+        const int n = w.q0 + i * kBM + row;
         if (n < p.n_q) {
-          for (int c = 0; c < D / 8; ++c)
-            reinterpret_cast<uint4*>(orow)[c] = make_uint4(0u, 0u, 0u, 0u);
-          if (p.lse != nullptr) p.lse[sr] = -INFINITY;
+          uint4* o4 = reinterpret_cast<uint4*>(
+              p.out + ((static_cast<int64_t>(w.b) * p.n_q + n) * p.H + w.h) * D + D / 2 * ch);
+          for (int c = 0; c < D / 16; ++c) o4[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (p.lse != nullptr && ch == 0)
+            p.lse[(static_cast<int64_t>(w.b) * p.H + w.h) * p.n_q + n] = -INFINITY;
         }
         continue;
       }
@@ -315,35 +406,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = 0.f, l = 0.f;
       for (int j = 0; j < w.nt; ++j, ++t) {
         ok = wait_all(s_full[i], t);
-        if (!ok) break;
         tc_fence_after();
-        uint32_t s[kBN];
-        tmem_ld128_wait(ts, s);
-        const int valid = w.len - j * kBN;
-        if (valid < kBN) {
-#pragma unroll
-          for (int c = 0; c < kBN; ++c)
-            if (c >= valid) s[c] = 0xff800000u;        // -infinity
+        const int valid = w.len - j * kBN - 64 * ch;     // of this thread's 64 states
+        uint32_t s[32];
+        float mx = -INFINITY;
+        if (ok) {
+          tmem_ld32_wait(ts + 32, s);
+          mx = masked_max(s, valid - 32);
+          tmem_ld32_wait(ts, s);
+          mx = fmaxf(mx, masked_max(s, valid)) * p.scale_log2;
         }
-        float mx;
-        {
-          float m8[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float a = fmax3(__uint_as_float(s[k]), __uint_as_float(s[k + 8]),
-                            __uint_as_float(s[k + 16]));
-#pragma unroll
-            for (int c = 24; c < kBN - 8; c += 16)
-              a = fmax3(a, __uint_as_float(s[c + k]), __uint_as_float(s[c + 8 + k]));
-            m8[k] = fmaxf(a, __uint_as_float(s[kBN - 8 + k]));
-          }
-          mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
-                     fmaxf(m8[6], m8[7])) * p.scale_log2;
-        }
-        if constexpr (!Sh::kAliasP) {
-          tc_fence_before();
-          mbar_arrive(smem_u32(&s_free[i]));
-        }
+        // The other half's maximum.  Every thread of the stream passes this barrier in every tile,
+        // and all of them leave here if a wait of one ran out.
+        *mine = mx;
+        tc_fence_before();
+        ok = !named_bar_or(1 + i, kStreamThreads, !ok);
+        if (!ok) break;
+        mx = fmaxf(mx, *other);
         float alpha = 1.f;
         bool rescale = false;
         if (j == 0) {
@@ -355,16 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = m_new;
           rescale = true;
         }
-        // with P in S's columns, S(j) came after PV(j-1); otherwise wait for that product before
-        // P's buffer or O is written
+        // O and P's buffer are free once PV(j-1) is complete; with P in S's columns QK(j) waited
         if (!Sh::kAliasP && t > 0) {
-          ok = wait_all(pv_done[i], t - 1);
-          if (!ok) break;
+          if (ok) ok = wait_all(pv_done[i], t - 1);
           tc_fence_after();
         }
         if (rescale) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
+          for (int c = 0; c < D / 2; c += 16) {
             uint32_t r[16];
             tmem_ld16_wait(to + c, r);
 #pragma unroll
@@ -372,55 +449,73 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(to + c, r);
           }
         }
-        if (valid < kBN && w.len < p.n_kv) {
-          // the value rows of masked states (both streams write the same zeros)
+        const bool ragged = w.len - j * kBN < kBN;
+        if (ragged && w.len < p.n_kv) {
+          // the value rows of this half's masked states (both streams write the same zeros)
           const uint32_t uv = u0 + 2 * j + 1;
-          ok = wait_all(kv_full[uv % kStages], uv / kStages);
-          if (!ok) break;
-          zero_rows<Sh::kBlocks>(sKV + (uv % kStages) * kTile, valid, row, kBM);
+          if (ok) ok = wait_all(kv_full[uv % kStages], uv / kStages);
+          zero_rows<Sh::kBlocks>(sKV + (uv % kStages) * kTile, 64 * ch + max(valid, 0),
+                                 64 * ch + 64, threadIdx.x % 128, 128);
           fence_proxy_async_smem();
         }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pw[32];
-          l += valid >= kBN ? exp_pairs<64, Sh::kPolyPairs>(s + 64 * half, p.scale_log2, m, pw)
-                            : exp_pairs<64, 0>(s + 64 * half, p.scale_log2, m, pw);
-#pragma unroll
-          for (int c = 0; c < 32; c += 16) {
-            uint32_t w16[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) w16[k] = pw[c + k];
-            tmem_st16(tp + 32 * half + c, w16);
-          }
-          tmem_wait_st();
+        uint32_t pw[16];
+        l += ragged ? exp_pairs<32, 0>(s, p.scale_log2, m, pw)
+                    : exp_pairs<32, Sh::kPolyPairs>(s, p.scale_log2, m, pw);
+        tmem_ld32_wait(ts + 32, s);
+        if constexpr (!Sh::kAliasP) {
           tc_fence_before();
-          mbar_arrive(smem_u32(&p_half[i][half]));
+          mbar_arrive(smem_u32(&s_free[i]));
         }
+        tmem_st16(tp, pw);
+        if (ragged) masked_max(s, valid - 32);
+        l += ragged ? exp_pairs<32, 0>(s, p.scale_log2, m, pw)
+                    : exp_pairs<32, Sh::kPolyPairs>(s, p.scale_log2, m, pw);
+        tmem_st16(tp + 16, pw);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&p_full[i][ch]));
       }
-      if (!ok) break;
+      if (!ok) break;       // (left at the barrier above, by every thread of the stream)
       u0 += 2 * w.nt;
       ok = wait_all(pv_done[i], t - 1);
-      if (!ok) break;
       tc_fence_after();
+      *mine = l;
+      ok = !named_bar_or(1 + i, kStreamThreads, !ok);
+      if (!ok) break;
+      l += *other;
       const float inv_l = 1.f / l;
-      if (p.lse != nullptr && n < p.n_q) p.lse[sr] = (m + log2f(l)) * kLn2;
+      const int n = w.q0 + i * kBM + row;
+      if (p.lse != nullptr && ch == 0 && n < p.n_q)
+        p.lse[(static_cast<int64_t>(w.b) * p.H + w.h) * p.n_q + n] = (m + log2f(l)) * kLn2;
+      // O / l over the item's Q tile, which its last product has read: 16-byte pieces of this row
+      // where a TMA copy with the 128-byte swizzle expects them
+      const uint32_t stage = sQ + (2 * i + (n_item & 1)) * kTile;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < D / 2; c += 32) {
         uint32_t r[32];
         tmem_ld32_wait(to + c, r);
-        uint32_t v[16];
+        const int col = D / 2 * ch + c;
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          v[k] = pack_bf16x2(__uint_as_float(r[2 * k]) * inv_l, __uint_as_float(r[2 * k + 1]) * inv_l);
-        if (n < p.n_q) {
-          uint4* d4 = reinterpret_cast<uint4*>(orow + c);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t v[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            d4[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          for (int e = 0; e < 4; ++e)
+            v[e] = pack_bf16x2(__uint_as_float(r[8 * k + 2 * e]) * inv_l,
+                               __uint_as_float(r[8 * k + 2 * e + 1]) * inv_l);
+          const uint32_t at = stage + (col / 64) * kBlk + row * 128 +
+                              ((((col % 64) / 8 + k) ^ (row & 7)) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+                       "r"(v[2]), "r"(v[3])
+                       : "memory");
         }
       }
       tc_fence_before();
       mbar_arrive(smem_u32(&o_free[i]));
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&o_staged[i]));
+      // the row sums are read before the next item's maxima take their place
+      named_bar_sync(1 + i, kStreamThreads);
+      ++n_item;
     }
   }
   tc_fence_before();
@@ -445,11 +540,12 @@ mla_status cross_tmap(CUtensorMap* m, const void* base, int B, int n, int heads,
 template <int D>
 mla_status fwd_impl(const CrossDims& d, const CrossArgs& a, cudaStream_t s) {
   using Sh = FwdShape<D>;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   mla_status st;
   if ((st = cross_tmap(&tq, a.q, d.B, d.n_q, d.H, D, d.q_row, kBM)) != MLA_OK) return st;
   if ((st = cross_tmap(&tk, a.k, d.B, d.n_kv, d.Hkv, D, d.k_row, kBN)) != MLA_OK) return st;
   if ((st = cross_tmap(&tv, a.v, d.B, d.n_kv, d.Hkv, D, d.v_row, kBN)) != MLA_OK) return st;
+  if ((st = cross_tmap(&to, a.out, d.B, d.n_q, d.H, D, d.H * D, kBM)) != MLA_OK) return st;
   CrossFwdParams p;
   p.n_q = d.n_q; p.H = d.H; p.rep = d.H / d.Hkv; p.n_kv = d.n_kv;
   p.pairs = ceil_div(d.n_q, 2 * kBM);
@@ -460,7 +556,7 @@ mla_status fwd_impl(const CrossDims& d, const CrossArgs& a, cudaStream_t s) {
   MLA_CUDA_TRY(cudaFuncSetAttribute(cross_fwd_tc_kernel<D>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem));
   MLA_CUDA_TRY(launch_pdl(cross_fwd_tc_kernel<D>, dim3(std::min(p.items, 148)), dim3(kThreads),
-                          Sh::kSmem, s, tq, tk, tv, p));
+                          Sh::kSmem, s, tq, tk, tv, to, p));
   return MLA_OK;
 }
 
