@@ -556,8 +556,9 @@ mla_status mla_attention_fwd_from_cq_q4(const mla_config* cfg, const void* c_q, 
  * aligned.  Results do not depend on the order in which blocks run: the same call gives the same
  * bits.
  *
- * dtype as in mla_config.  kernel_path: MLA_PATH_AUTO or MLA_PATH_SIMT (CUDA cores).  d_head <=
- * 256.  Outputs must not overlap inputs.  dev_status as in mla_attention_fwd.
+ * dtype as in mla_config.  kernel_path: MLA_PATH_AUTO (tensor cores for bf16 with d_head 64 or
+ * 128, CUDA cores otherwise) or MLA_PATH_SIMT (CUDA cores).  d_head <= 256.  Outputs must not
+ * overlap inputs.  dev_status as in mla_attention_fwd.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (d_head above 256), MLA_ERR_ALIGNMENT,
  * MLA_ERR_WORKSPACE, MLA_ERR_CUDA.
  * ------------------------------------------------------------------------------------------ */

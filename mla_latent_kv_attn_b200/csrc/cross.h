@@ -57,8 +57,10 @@ mla_status cross_bwd_simt(const CrossDims& d, const CrossBwdArgs& a, float* delt
 mla_status cross_delta(const CrossDims& d, const void* out, const void* d_out, float* delta,
                        cudaStream_t s);
 
-// Tensor-core kernels: bf16 with d 64 or 128 (cross_sm100.cu).
+// Tensor-core kernels: bf16 with d 64 or 128 (cross_sm100.cu, cross_bwd_sm100.cu).
 bool cross_tc_supported(const CrossDims& d);
 mla_status cross_fwd_tc(const CrossDims& d, const CrossArgs& a, cudaStream_t s);
+size_t cross_bwd_tc_workspace(const CrossDims& d);
+mla_status cross_bwd_tc(const CrossDims& d, const CrossBwdArgs& a, void* workspace, cudaStream_t s);
 
 }  // namespace mla

@@ -1,0 +1,840 @@
+// cross_bwd_sm100.cu - the gradients of the cross attention on the sm_100a tensor cores, for bf16
+// with head widths 64 and 128 (the mathematics are in cross_simt.cu).  Four launches:
+//
+//   stats   per query row lse log2(e) and delta = g . o, in arrays padded to whole 128-row tiles (a
+//           padding row's lse is +infinity, so that its probabilities are zero)
+//   dQ      a 128-row query tile per item, streaming the states' tiles:
+//             S = Q K_j^T, dP = G V_j^T, dS = P o (dP - delta) scale, dQ += dS K_j
+//   dK, dV  a 128-row tile of states per block, streaming the query tiles of the heads that share
+//           it:  S^T = K Q_i^T, dP^T = V G_i^T, dV += P^T G_i, dK += dS^T Q_i
+//   reduce  the blocks' sums of one tile of states added in a fixed order and rounded once
+//
+// S and dP are computed twice (7 products where 5 would do): a single pass would have to add dQ
+// over blocks, in an order that changes from run to run or in fp32 copies that cost more memory
+// traffic than the two products (115 MB for 4680 queries, 12 heads and 512 states).
+// P and dS are rounded to bf16 as operands; every product accumulates in fp32 in TMEM, where P and
+// dS also take the place of S and dP: a thread that has read 64 columns of scores writes 32 columns
+// of bf16 pairs over them.  Every wait is bounded; one that runs out writes MLA_ERR_DEVICE_TIMEOUT
+// to dev_status.
+#include "cross_tc.cuh"
+
+namespace mla {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kT = kCrossTile;            // rows of every tile
+constexpr int kSoftmaxThreads = 256;      // two threads per row, each with half of the columns
+constexpr int kProducerWarp = 8;
+constexpr int kIssuerA = 9, kIssuerB = 10;
+constexpr int kStoreWarp = 11;
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kPolyPairs = 2;             // pairs of 8 whose exponential comes from the polynomial
+
+struct CrossBwdParams {
+  int B, H, Hkv, rep, n_q, n_kv, n_pad;   // n_pad: n_q rounded up to whole tiles
+  int q_tiles, items;                     // dQ: items of one query tile
+  int kv_tiles, splits;                   // dK, dV: blocks that share a tile's queries
+  float scale, scale_log2;
+  const int32_t* kv_len;
+  const float* lse2;                      // [B, H, n_pad]
+  const float* delta;                     // [B, H, n_pad]
+  float* partial;                         // [2, splits, B, Hkv, kv_tiles, D/4, 128, 4]
+  int32_t* dev_status;
+};
+
+// p = 2^(s scale - l) of 32 columns of a row whose l is the same (dQ) or that of the column (dK, dV,
+// l2 then holds 16 pairs); kPoly: some exponentials by the polynomial.
+template <bool kPoly>
+__device__ __forceinline__ void probabilities(const uint32_t (&s)[32], uint64_t scale2,
+                                              const uint64_t* neg_l2, int l_step, float* p) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), scale2,
+                     neg_l2[k * l_step]),
+              x0, x1);
+    if (kPoly && (k & 7) < kPolyPairs) {
+      exp2_poly_pair(x0, x1, p[2 * k], p[2 * k + 1]);
+    } else {
+      p[2 * k] = fast_exp2(x0);
+      p[2 * k + 1] = fast_exp2(x1);
+    }
+  }
+}
+
+// dS = p (dP scale - delta scale) of 32 columns, as bf16 pairs.
+__device__ __forceinline__ void score_gradients(const uint32_t (&dp)[32], const float* p,
+                                                uint64_t scale2, const uint64_t* neg_d2, int d_step,
+                                                uint32_t (&w)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    float d0, d1;
+    f2_unpack(f2_mul(f2_fma(f2_pack(__uint_as_float(dp[2 * k]), __uint_as_float(dp[2 * k + 1])),
+                            scale2, neg_d2[k * d_step]),
+                     f2_pack(p[2 * k], p[2 * k + 1])),
+              d0, d1);
+    w[k] = pack_bf16x2(d0, d1);
+  }
+}
+
+// acc (+)= A B with A [128, 128] as bf16 pairs in TMEM, each half of its columns in the first 32 of
+// 64 columns from `a` on, and B [128, D] a tile read MN-major.
+template <int D>
+__device__ __forceinline__ void mma_pairs_by_tile(uint32_t acc, uint32_t a, uint32_t tile,
+                                                  bool accumulate) {
+  constexpr uint32_t idesc = idesc_bf16_f32(kT, D, 0, 1);
+  const uint64_t b = smem_desc(tile, kT * 128, 1024, kSwizzle128B);
+#pragma unroll
+  for (int kk = 0; kk < kT / 16; ++kk)
+    mma_ts(acc, a + 64 * (kk >> 2) + 8 * (kk & 3), b + 128 * kk, idesc,
+           (accumulate || kk) ? 1u : 0u);
+}
+
+// d = A B^T of two K-major tiles [128, D] in shared memory.
+template <int D>
+__device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a_tile, uint32_t b_tile) {
+  constexpr uint32_t idesc = idesc_bf16_f32(kT, kT, 0, 0);
+  const uint64_t a = smem_desc(a_tile, 16, 1024, kSwizzle128B);
+  const uint64_t b = smem_desc(b_tile, 16, 1024, kSwizzle128B);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = ((kk >> 2) * kT * 128 >> 4) + 2 * (kk & 3);
+    mma_ss(d, a + off, b + off, idesc, kk ? 1u : 0u);
+  }
+}
+
+// One thread: the tile of rows [row, row + 128) of head h of sample b.
+template <int D>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int h,
+                                          int row, int b) {
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k)
+    tma_load_4d(dst + k * kT * 128, map, bar, 64 * k, h, row, b);
+}
+
+// ------------------------------------------------------------------------------------- stats
+
+// One block per 64 rows of one head: 16 lanes read a row (8 or 4 values each).
+constexpr int kStatRows = 64;
+
+template <int D>
+__global__ void __launch_bounds__(256)
+    cross_stats_kernel(const bf16* __restrict__ out, const bf16* __restrict__ g,
+                       const float* __restrict__ lse, float* __restrict__ lse2,
+                       float* __restrict__ delta, int H, int n_q, int n_pad) {
+  grid_dep_wait();
+  grid_dep_launch();
+  constexpr int kPer = D / 16;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int64_t bh = static_cast<int64_t>(b) * H + h;
+  const int l16 = threadIdx.x % 16;
+#pragma unroll
+  for (int r0 = 0; r0 < kStatRows; r0 += 16) {
+    const int i = blockIdx.x * kStatRows + r0 + threadIdx.x / 16;
+    float s = 0.f;
+    if (i < n_q) {
+      const int64_t at = ((static_cast<int64_t>(b) * n_q + i) * H + h) * D + l16 * kPer;
+      uint32_t x[kPer / 2], y[kPer / 2];
+      if constexpr (D == 128) {
+        *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(out + at);
+        *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(g + at);
+      } else {
+        *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(out + at);
+        *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(g + at);
+      }
+#pragma unroll
+      for (int k = 0; k < kPer / 2; ++k) {
+        // a bf16 is the upper half of its float
+        s = fmaf(__uint_as_float(x[k] << 16), __uint_as_float(y[k] << 16), s);
+        s = fmaf(__uint_as_float(x[k] & 0xffff0000u), __uint_as_float(y[k] & 0xffff0000u), s);
+      }
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (l16 == 0 && i < n_pad) {
+      lse2[bh * n_pad + i] = i < n_q ? lse[bh * n_q + i] * kLog2e : INFINITY;
+      delta[bh * n_pad + i] = s;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------- dQ
+
+template <int D_>
+struct DqShape {
+  static constexpr int D = D_;
+  static constexpr int kTile = kT * D * 2;
+  static constexpr int kKStages = D == 128 ? 2 : 4;
+  static constexpr int kVStages = D == 128 ? 1 : 3;
+  static constexpr int kTiles = 4 + kKStages + kVStages;      // Q and G twice, then the rings
+  static constexpr int kSmem = kTiles * kTile + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+constexpr uint32_t kDqColS = 0, kDqColDP = 128, kDqColAcc = 384;    // dP twice
+
+template <int kKStages, int kVStages>
+struct DqShared {
+  uint64_t qg_full[2], qg_empty[2];       // Q and G of an item (by parity)
+  uint64_t k_full[kKStages], k_empty[kKStages];
+  uint64_t v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full, s_free;                // S(j) complete; read
+  uint64_t dp_full[2], dq_done[2];        // dP(j) complete; the product with dS(j) complete
+  uint64_t ds_full;                       // dS(j) in TMEM
+  uint64_t acc_free;                      // the item's dQ is in registers
+  uint64_t staged;                        // and in its Q buffer
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+struct DqItem {
+  int b, h, q0, len, nt;
+};
+
+__device__ __forceinline__ DqItem dq_item(const CrossBwdParams& p, int it) {
+  DqItem w;
+  w.q0 = (it % p.q_tiles) * kT;
+  const int bh = it / p.q_tiles;
+  w.h = bh % p.H;
+  w.b = bh / p.H;
+  w.len = cross_len(p.kv_len, w.b, p.n_kv);
+  w.nt = ceil_div(w.len, kT);
+  return w;
+}
+
+// Roles (384 threads): warps 0-7 softmax (warps w and w + 4 share 32 rows, each half of the
+// columns), 8 TMA producer, 9 issuer of S, 10 issuer of dP and dQ, 11 TMA stores of dQ.  The two dP
+// buffers let dP(j+1) run under the softmax of j, and S(j+1) runs once S(j) has been read.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_g,
+                       const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_dq, bf16* __restrict__ d_q,
+                       CrossBwdParams p) {
+  using Sh = DqShape<D>;
+  constexpr int kTile = Sh::kTile, kKStages = Sh::kKStages, kVStages = Sh::kVStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t sQ = smem_u32(smem_raw), sG = sQ + 2 * kTile, sK = sG + 2 * kTile;
+  const uint32_t sV = sK + kKStages * kTile;
+  auto& sh = *reinterpret_cast<DqShared<kKStages, kVStages>*>(smem_raw + Sh::kTiles * kTile);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  volatile int* abort_flag = &sh.abort_flag;
+
+  if (threadIdx.x == 0) {
+    sh.abort_flag = 0;
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&sh.qg_full[b]), 1);
+      mbar_init(smem_u32(&sh.qg_empty[b]), 1);
+      mbar_init(smem_u32(&sh.dp_full[b]), 1);
+      mbar_init(smem_u32(&sh.dq_done[b]), 1);
+    }
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(smem_u32(&sh.k_full[s]), 1);
+      mbar_init(smem_u32(&sh.k_empty[s]), 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(smem_u32(&sh.v_full[s]), 1);
+      mbar_init(smem_u32(&sh.v_empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sh.s_full), 1);
+    mbar_init(smem_u32(&sh.s_free), kSoftmaxThreads);
+    mbar_init(smem_u32(&sh.ds_full), kSoftmaxThreads);
+    mbar_init(smem_u32(&sh.acc_free), kSoftmaxThreads);
+    mbar_init(smem_u32(&sh.staged), kSoftmaxThreads);
+    fence_barrier_init();
+  }
+  if (warp == kIssuerA) {
+    tmem_alloc(smem_u32(&sh.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  grid_dep_wait();
+  grid_dep_launch();
+
+  const auto wait = [&](uint64_t& bar, uint32_t phase) {
+    return mbar_wait_or_abort(smem_u32(&bar), phase & 1, abort_flag, p.dev_status);
+  };
+
+  if (warp == kProducerWarp) {
+    if (lane == 0) {
+      uint32_t n = 0, t = 0;              // items, tiles
+      bool ok = true;
+      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+        const DqItem w = dq_item(p, it);
+        if (w.nt == 0) continue;
+        const int b = n & 1;
+        ok = wait(sh.qg_empty[b], (n >> 1) + 1);
+        if (!ok) break;
+        const uint32_t qb = smem_u32(&sh.qg_full[b]);
+        mbar_arrive_expect_tx(qb, 2 * kTile);
+        load_tile<D>(sQ + b * kTile, &tm_q, qb, w.h, w.q0, w.b);
+        load_tile<D>(sG + b * kTile, &tm_g, qb, w.h, w.q0, w.b);
+        ++n;
+        for (int j = 0; j < w.nt && ok; ++j, ++t) {
+          const int ks = t % kKStages, vs = t % kVStages;
+          ok = wait(sh.k_empty[ks], t / kKStages + 1);
+          if (!ok) break;
+          const uint32_t kb = smem_u32(&sh.k_full[ks]);
+          mbar_arrive_expect_tx(kb, kTile);
+          load_tile<D>(sK + ks * kTile, &tm_k, kb, w.h / p.rep, j * kT, w.b);
+          ok = wait(sh.v_empty[vs], t / kVStages + 1);
+          if (!ok) break;
+          const uint32_t vb = smem_u32(&sh.v_full[vs]);
+          mbar_arrive_expect_tx(vb, kTile);
+          load_tile<D>(sV + vs * kTile, &tm_v, vb, w.h / p.rep, j * kT, w.b);
+        }
+      }
+    }
+  } else if (warp == kIssuerA) {
+    if (lane == 0) {
+      uint32_t n = 0, t = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+        const DqItem w = dq_item(p, it);
+        if (w.nt == 0) continue;
+        ok = wait(sh.qg_full[n & 1], n >> 1);
+        for (int j = 0; j < w.nt && ok; ++j, ++t) {
+          ok = wait(sh.k_full[t % kKStages], t / kKStages) && (t == 0 || wait(sh.s_free, t - 1));
+          if (!ok) break;
+          tc_fence_after();
+          mma_tiles<D>(tmem + kDqColS, sQ + (n & 1) * kTile, sK + (t % kKStages) * kTile);
+          mma_commit(smem_u32(&sh.s_full));
+        }
+        ++n;
+      }
+    }
+  } else if (warp == kIssuerB) {
+    if (lane == 0) {
+      uint32_t n = 0, t = 0;
+      bool ok = true;
+      // dP of tile u (of item n) into buffer u & 1, which the product with dS(u-2) has read
+      const auto issue_dp = [&](uint32_t u) {
+        if (!wait(sh.v_full[u % kVStages], u / kVStages) ||
+            (u >= 2 && !wait(sh.dq_done[u & 1], (u >> 1) - 1)))
+          return false;
+        tc_fence_after();
+        mma_tiles<D>(tmem + kDqColDP + 128 * (u & 1), sG + (n & 1) * kTile,
+                     sV + (u % kVStages) * kTile);
+        mma_commit(smem_u32(&sh.v_empty[u % kVStages]));
+        mma_commit(smem_u32(&sh.dp_full[u & 1]));
+        return true;
+      };
+      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+        const DqItem w = dq_item(p, it);
+        if (w.nt == 0) continue;
+        ok = wait(sh.qg_full[n & 1], n >> 1) && issue_dp(t);
+        for (int j = 0; j < w.nt && ok; ++j, ++t) {
+          if (j + 1 < w.nt) ok = issue_dp(t + 1);
+          ok = ok && wait(sh.ds_full, t) && (j > 0 || n == 0 || wait(sh.acc_free, n - 1));
+          if (!ok) break;
+          tc_fence_after();
+          mma_pairs_by_tile<D>(tmem + kDqColAcc, tmem + kDqColDP + 128 * (t & 1),
+                               sK + (t % kKStages) * kTile, j > 0);
+          mma_commit(smem_u32(&sh.k_empty[t % kKStages]));
+          mma_commit(smem_u32(&sh.dq_done[t & 1]));
+        }
+        ++n;
+      }
+    }
+  } else if (warp == kStoreWarp) {
+    if (lane == 0) {
+      uint32_t n = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+        const DqItem w = dq_item(p, it);
+        if (w.nt == 0) continue;
+        ok = wait(sh.staged, n);
+        if (!ok) break;
+        for (int k = 0; k < D / 64; ++k)           // (rows past n_q are not written)
+          tma_store_4d(&tm_dq, sQ + (n & 1) * kTile + k * kT * 128, 64 * k, w.h, w.q0, w.b);
+        bulk_commit_group();
+        bulk_wait_group_read<0>();
+        mbar_arrive(smem_u32(&sh.qg_empty[n & 1]));
+        ++n;
+      }
+      bulk_wait_group_all();
+    }
+  } else {
+    const int ch = warp / 4, row = (warp % 4) * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+    const uint32_t ts = tl + kDqColS + 64 * ch;
+    const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2);
+    const auto wait_all = [&](uint64_t& bar, uint32_t phase) {
+      return __all_sync(0xffffffffu, wait(bar, phase)) != 0;
+    };
+    uint32_t n = 0, t = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+      const DqItem w = dq_item(p, it);
+      if (w.nt == 0) {
+        const int i = w.q0 + row;
+        if (i < p.n_q) {
+          uint4* o4 = reinterpret_cast<uint4*>(
+              d_q + ((static_cast<int64_t>(w.b) * p.n_q + i) * p.H + w.h) * D + D / 2 * ch);
+          for (int c = 0; c < D / 16; ++c) o4[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      const int64_t sr = (static_cast<int64_t>(w.b) * p.H + w.h) * p.n_pad + w.q0 + row;
+      const float nl = -p.lse2[sr];
+      // a single state's softmax is constant: its dS is zero
+      const float sc = w.len == 1 ? 0.f : p.scale, nd = -p.delta[sr] * sc;
+      const uint64_t nl2 = f2_pack(nl, nl), sc2 = f2_pack(sc, sc), nd2 = f2_pack(nd, nd);
+      for (int j = 0; j < w.nt; ++j, ++t) {
+        ok = wait_all(sh.s_full, t);
+        if (!ok) break;
+        tc_fence_after();
+        const int valid = w.len - j * kT - 64 * ch;
+        float pr[64];
+        {
+          uint32_t s[32];
+          tmem_ld32_wait(ts, s);
+          probabilities<true>(s, sl2, &nl2, 0, pr);
+          tmem_ld32_wait(ts + 32, s);
+          tc_fence_before();
+          mbar_arrive(smem_u32(&sh.s_free));
+          probabilities<true>(s, sl2, &nl2, 0, pr + 32);
+        }
+        ok = wait_all(sh.dp_full[t & 1], t >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t td = tl + kDqColDP + 128 * (t & 1) + 64 * ch;
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t dp[32], ds[16];
+          tmem_ld32_wait(td + c, dp);
+          score_gradients(dp, pr + c, sc2, &nd2, 0, ds);
+          if (valid < c + 32) {
+            // masked states, whatever their scores and dP hold
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              if (c + 2 * k >= valid) ds[k] = 0u;
+              else if (c + 2 * k + 1 >= valid) ds[k] &= 0xffffu;
+            }
+          }
+          tmem_st16(td + c / 2, ds);
+        }
+        if (w.len - j * kT < kT && w.len < p.n_kv) {
+          // the product reads the keys of masked states: this half's rows become zeros
+          zero_rows<D / 64>(sK + (t % kKStages) * kTile, 64 * ch + max(valid, 0), 64 * ch + 64,
+                            threadIdx.x % 128, 128);
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sh.ds_full));
+      }
+      if (!ok) break;
+      ok = wait_all(sh.dq_done[(t - 1) & 1], (t - 1) >> 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t stage = sQ + (n & 1) * kTile;
+#pragma unroll 1
+      for (int c = 0; c < D / 2; c += 32) {
+        uint32_t r[32];
+        const int col = D / 2 * ch + c;
+        tmem_ld32_wait(tl + kDqColAcc + col, r);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = pack_bf16x2(__uint_as_float(r[8 * k + 2 * e]), __uint_as_float(r[8 * k + 2 * e + 1]));
+          store_shared16(swizzled_piece(stage + (col / 64) * kT * 128, row, (col % 64) / 8 + k), v);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sh.acc_free));
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&sh.staged));
+      ++n;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssuerA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------------------------- dK, dV
+
+template <int D_>
+struct DkvShape {
+  static constexpr int D = D_;
+  static constexpr int kTile = kT * D * 2;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kTiles = 2 + 2 * kStages;              // K, V, then Q and G of each stage
+  static constexpr int kStatBytes = 2 * kT * 4;               // lse2 and delta of a query tile
+  static constexpr int kSmem = kTiles * kTile + kStages * kStatBytes + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+constexpr uint32_t kColS = 0, kColDP = 128, kColDK = 256, kColDV = 384;
+
+template <int kStages>
+struct DkvShared {
+  uint64_t k_full, v_full;
+  uint64_t q_full[kStages], q_empty[kStages];    // Q_i and its statistics
+  uint64_t g_full[kStages], g_empty[kStages];
+  uint64_t s_full, dp_full;        // S^T, dP^T complete
+  uint64_t p_full, ds_full;        // P^T, dS^T in TMEM
+  uint64_t dv_done, dk_done;       // the products that read them complete
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// A block per split, state tile, key head and sample.  Roles (352 threads): warps 0-7 softmax, 8 TMA
+// producer, 9 issuer of S^T and dV, 10 issuer of dP^T and dK.  S^T(i+1) may run once dV(i) has read
+// P^T(i), which the softmax writes before it turns to dS: while dS(i) is being computed the tensor
+// cores have dV(i) and S^T(i+1), and while P(i+1) is, dK(i) and dP^T(i+1).
+// Rows of masked states hold whatever their scores gave; they reach no other row and are not used.
+constexpr int kThreadsKV = 352;
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsKV, 1)
+    cross_dkv_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
+                        const __grid_constant__ CUtensorMap tm_g,
+                        const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, CrossBwdParams p) {
+  using Sh = DkvShape<D>;
+  constexpr int kTile = Sh::kTile, kStages = Sh::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t sK = smem_u32(smem_raw), sV = sK + kTile, sQ = sV + kTile;
+  const uint32_t sG = sQ + kStages * kTile, sStat = sG + kStages * kTile;
+  const float* stats = reinterpret_cast<const float*>(smem_raw + Sh::kTiles * kTile);
+  auto& sh = *reinterpret_cast<DkvShared<kStages>*>(smem_raw + Sh::kTiles * kTile +
+                                                    kStages * Sh::kStatBytes);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int split = blockIdx.x % p.splits, bt = blockIdx.x / p.splits;
+  const int tile = bt % p.kv_tiles, kh = bt / p.kv_tiles % p.Hkv, b = bt / p.kv_tiles / p.Hkv;
+  volatile int* abort_flag = &sh.abort_flag;
+
+  if (threadIdx.x == 0) {
+    sh.abort_flag = 0;
+    mbar_init(smem_u32(&sh.k_full), 1);
+    mbar_init(smem_u32(&sh.v_full), 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&sh.q_full[s]), 1);
+      mbar_init(smem_u32(&sh.q_empty[s]), 1);
+      mbar_init(smem_u32(&sh.g_full[s]), 1);
+      mbar_init(smem_u32(&sh.g_empty[s]), 2);      // dP^T and dV
+    }
+    mbar_init(smem_u32(&sh.s_full), 1);
+    mbar_init(smem_u32(&sh.dp_full), 1);
+    mbar_init(smem_u32(&sh.p_full), kSoftmaxThreads);
+    mbar_init(smem_u32(&sh.ds_full), kSoftmaxThreads);
+    mbar_init(smem_u32(&sh.dv_done), 1);
+    mbar_init(smem_u32(&sh.dk_done), 1);
+    fence_barrier_init();
+  }
+  if (warp == kIssuerA) {
+    tmem_alloc(smem_u32(&sh.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  grid_dep_wait();
+  grid_dep_launch();
+
+  const auto wait = [&](uint64_t& bar, uint32_t phase) {
+    return mbar_wait_or_abort(smem_u32(&bar), phase & 1, abort_flag, p.dev_status);
+  };
+  const int len = cross_len(p.kv_len, b, p.n_kv);
+  // this block's share of the (head, query tile) pairs: none for a tile of masked states
+  const int work = p.rep * p.q_tiles;
+  const int first = static_cast<int>(static_cast<int64_t>(work) * split / p.splits);
+  const int n = tile * kT < len
+                    ? static_cast<int>(static_cast<int64_t>(work) * (split + 1) / p.splits) - first
+                    : 0;
+
+  if (n == 0) {
+    // (falls through to the end: nothing is written, the sum skips masked tiles)
+  } else if (warp == kProducerWarp) {
+    if (lane == 0) {
+      const uint32_t kb = smem_u32(&sh.k_full), vb = smem_u32(&sh.v_full);
+      mbar_arrive_expect_tx(kb, kTile);
+      load_tile<D>(sK, &tm_k, kb, kh, tile * kT, b);
+      bool ok = true;
+      for (int i = 0; i < n && ok; ++i) {
+        const int s = i % kStages;
+        const int h = kh * p.rep + (first + i) / p.q_tiles, q0 = (first + i) % p.q_tiles * kT;
+        ok = wait(sh.q_empty[s], i / kStages + 1);
+        if (!ok) break;
+        const uint32_t qb = smem_u32(&sh.q_full[s]);
+        const uint32_t st = sStat + s * Sh::kStatBytes;
+        const int64_t so = (static_cast<int64_t>(b) * p.H + h) * p.n_pad + q0;
+        mbar_arrive_expect_tx(qb, kTile + Sh::kStatBytes);
+        load_tile<D>(sQ + s * kTile, &tm_q, qb, h, q0, b);
+        bulk_load(st, p.lse2 + so, kT * 4, qb);
+        bulk_load(st + kT * 4, p.delta + so, kT * 4, qb);
+        if (i == 0) {
+          mbar_arrive_expect_tx(vb, kTile);
+          load_tile<D>(sV, &tm_v, vb, kh, tile * kT, b);
+        }
+        ok = wait(sh.g_empty[s], i / kStages + 1);
+        if (!ok) break;
+        const uint32_t gb = smem_u32(&sh.g_full[s]);
+        mbar_arrive_expect_tx(gb, kTile);
+        load_tile<D>(sG + s * kTile, &tm_g, gb, h, q0, b);
+      }
+    }
+  } else if (warp == kIssuerA) {
+    if (lane == 0) {
+      bool ok = wait(sh.k_full, 0);
+      for (int i = 0; i < n && ok; ++i) {
+        const int s = i % kStages;
+        ok = wait(sh.q_full[s], i / kStages) && (i == 0 || wait(sh.dv_done, i - 1));
+        if (!ok) break;
+        tc_fence_after();
+        mma_tiles<D>(tmem + kColS, sK, sQ + s * kTile);
+        mma_commit(smem_u32(&sh.s_full));
+        ok = wait(sh.g_full[s], i / kStages) && wait(sh.p_full, i);
+        if (!ok) break;
+        tc_fence_after();
+        mma_pairs_by_tile<D>(tmem + kColDV, tmem + kColS, sG + s * kTile, i > 0);
+        mma_commit(smem_u32(&sh.g_empty[s]));
+        mma_commit(smem_u32(&sh.dv_done));
+      }
+    }
+  } else if (warp == kIssuerB) {
+    if (lane == 0) {
+      bool ok = wait(sh.v_full, 0);
+      for (int i = 0; i < n && ok; ++i) {
+        const int s = i % kStages;
+        ok = wait(sh.g_full[s], i / kStages) && (i == 0 || wait(sh.dk_done, i - 1));
+        if (!ok) break;
+        tc_fence_after();
+        mma_tiles<D>(tmem + kColDP, sV, sG + s * kTile);
+        mma_commit(smem_u32(&sh.g_empty[s]));
+        mma_commit(smem_u32(&sh.dp_full));
+        ok = wait(sh.ds_full, i);
+        if (!ok) break;
+        tc_fence_after();
+        mma_pairs_by_tile<D>(tmem + kColDK, tmem + kColDP, sQ + s * kTile, i > 0);
+        mma_commit(smem_u32(&sh.q_empty[s]));
+        mma_commit(smem_u32(&sh.dk_done));
+      }
+    }
+  } else {
+    const int ch = warp / 4, row = (warp % 4) * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+    const uint32_t ts = tl + kColS + 64 * ch, td = tl + kColDP + 64 * ch;
+    // a single state's softmax is constant: its dS is zero
+    const float sc = len == 1 ? 0.f : p.scale;
+    const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2), sc2 = f2_pack(sc, sc);
+    const uint64_t neg2 = f2_pack(-1.f, -1.f), nsc2 = f2_pack(-sc, -sc);
+    const auto wait_all = [&](uint64_t& bar, uint32_t phase) {
+      return __all_sync(0xffffffffu, wait(bar, phase)) != 0;
+    };
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int s = i % kStages;
+      // (the statistics came with the loads of q_full)
+      ok = wait_all(sh.q_full[s], i / kStages) && wait_all(sh.s_full, i);
+      if (!ok) break;
+      tc_fence_after();
+      const float4* lse4 =
+          reinterpret_cast<const float4*>(stats + s * (Sh::kStatBytes / 4) + 64 * ch);
+      const float4* del4 = lse4 + kT / 4;
+      float pr[64];
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t sc32[32], pw[16];
+        uint64_t nl2[16];
+        tmem_ld32_wait(ts + c, sc32);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 l = lse4[c / 4 + k];
+          nl2[2 * k] = f2_mul(f2_pack(l.x, l.y), neg2);
+          nl2[2 * k + 1] = f2_mul(f2_pack(l.z, l.w), neg2);
+        }
+        probabilities<true>(sc32, sl2, nl2, 1, pr + c);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) pw[k] = pack_bf16x2(pr[c + 2 * k], pr[c + 2 * k + 1]);
+        tmem_st16(ts + c / 2, pw);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sh.p_full));
+      ok = wait_all(sh.dp_full, i);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t dp[32], ds[16];
+        uint64_t nd2[16];
+        tmem_ld32_wait(td + c, dp);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 d = del4[c / 4 + k];
+          nd2[2 * k] = f2_mul(f2_pack(d.x, d.y), nsc2);
+          nd2[2 * k + 1] = f2_mul(f2_pack(d.z, d.w), nsc2);
+        }
+        score_gradients(dp, pr + c, sc2, nd2, 1, ds);
+        tmem_st16(td + c / 2, ds);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sh.ds_full));
+    }
+    if (ok) ok = wait_all(sh.dv_done, n - 1) && wait_all(sh.dk_done, n - 1);
+    if (ok) {
+      tc_fence_after();
+      // four columns of 32 rows are 512 consecutive bytes
+      const int64_t tile_at =
+          (((static_cast<int64_t>(split) * p.B + b) * p.Hkv + kh) * p.kv_tiles + tile) * (kT * D);
+      const int64_t half = static_cast<int64_t>(p.splits) * p.B * p.Hkv * p.kv_tiles * (kT * D);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t r[32];
+        tmem_ld32_wait(tl + (ch == 0 ? kColDK : kColDV) + c, r);
+        float4* dst = reinterpret_cast<float4*>(p.partial + ch * half + tile_at) + (c / 4) * kT + row;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          dst[k * kT] = make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
+                                    __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssuerA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Sum over the splits, in order, of 16 columns of one row: a thread.  Rows of masked states are 0.
+template <int D>
+__global__ void __launch_bounds__(kT)
+    cross_dkv_reduce_kernel(bf16* __restrict__ d_k, bf16* __restrict__ d_v, CrossBwdParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int c16 = blockIdx.x % (D / 16), which = blockIdx.x / (D / 16) % 2;
+  const int bt = blockIdx.x / (D / 8);
+  const int tile = bt % p.kv_tiles, kh = bt / p.kv_tiles % p.Hkv, b = bt / p.kv_tiles / p.Hkv;
+  const int j = tile * kT + threadIdx.x;
+  if (j >= p.n_kv) return;
+  const int len = cross_len(p.kv_len, b, p.n_kv);
+  float4 a[4] = {};
+  if (j < len) {
+    const int64_t half = static_cast<int64_t>(p.B) * p.Hkv * p.kv_tiles * (kT * D);
+    const float4* src = reinterpret_cast<const float4*>(
+        p.partial + which * p.splits * half +
+        ((static_cast<int64_t>(b) * p.Hkv + kh) * p.kv_tiles + tile) * (kT * D)) +
+        4 * c16 * kT + threadIdx.x;
+    for (int s = 0; s < p.splits; ++s, src += half / 4) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = src[k * kT];
+        a[k].x += v.x; a[k].y += v.y; a[k].z += v.z; a[k].w += v.w;
+      }
+    }
+  }
+  uint4 o[2];
+  o[0] = make_uint4(pack_bf16x2(a[0].x, a[0].y), pack_bf16x2(a[0].z, a[0].w),
+                    pack_bf16x2(a[1].x, a[1].y), pack_bf16x2(a[1].z, a[1].w));
+  o[1] = make_uint4(pack_bf16x2(a[2].x, a[2].y), pack_bf16x2(a[2].z, a[2].w),
+                    pack_bf16x2(a[3].x, a[3].y), pack_bf16x2(a[3].z, a[3].w));
+  uint4* dst = reinterpret_cast<uint4*>(
+      (which ? d_v : d_k) + ((static_cast<int64_t>(b) * p.n_kv + j) * p.Hkv + kh) * D + 16 * c16);
+  dst[0] = o[0];
+  dst[1] = o[1];
+}
+
+// Blocks per tile of states: of the counts that give every block at least one query tile, the one
+// whose waves of 148 blocks take the fewest steps (a block costs about three steps beside its query
+// tiles), the smallest on a tie: each more adds sums to write and read.
+int dkv_splits(int tiles, int work) {
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int s = 1; s <= std::min(work, 16); ++s) {
+    const int64_t waves = (static_cast<int64_t>(tiles) * s + 147) / 148;
+    const int64_t cost = waves * (ceil_div(work, s) + 3);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+struct BwdLayout {
+  int n_pad, kv_tiles, splits;
+  size_t lse2, delta, partial, bytes;      // offsets of the three arrays, and their end
+};
+
+BwdLayout bwd_layout(const CrossDims& d) {
+  BwdLayout l;
+  l.n_pad = round_up(d.n_q, kT);
+  l.kv_tiles = ceil_div(d.n_kv, kT);
+  l.splits = dkv_splits(d.B * d.Hkv * l.kv_tiles, d.H / d.Hkv * (l.n_pad / kT));
+  const size_t stat = static_cast<size_t>(d.B) * d.H * l.n_pad * sizeof(float);   // 512-byte rows
+  l.lse2 = 0;
+  l.delta = stat;
+  l.partial = 2 * stat;
+  l.bytes = l.partial + 2 * static_cast<size_t>(l.splits) * d.B * d.Hkv * l.kv_tiles * kT * d.d *
+                            sizeof(float);
+  return l;
+}
+
+template <int D>
+mla_status bwd_impl(const CrossDims& d, const CrossBwdArgs& a, void* workspace, cudaStream_t s) {
+  const BwdLayout l = bwd_layout(d);
+  char* ws = static_cast<char*>(workspace);
+  CUtensorMap tq, tg, tk, tv, tdq;
+  mla_status st;
+  if ((st = cross_tmap(&tq, a.q, d.B, d.n_q, d.H, D, d.q_row, kT)) != MLA_OK) return st;
+  if ((st = cross_tmap(&tg, a.d_out, d.B, d.n_q, d.H, D, d.H * D, kT)) != MLA_OK) return st;
+  if ((st = cross_tmap(&tk, a.k, d.B, d.n_kv, d.Hkv, D, d.k_row, kT)) != MLA_OK) return st;
+  if ((st = cross_tmap(&tv, a.v, d.B, d.n_kv, d.Hkv, D, d.v_row, kT)) != MLA_OK) return st;
+  if ((st = cross_tmap(&tdq, a.d_q, d.B, d.n_q, d.H, D, d.H * D, kT)) != MLA_OK) return st;
+  CrossBwdParams p;
+  p.B = d.B; p.H = d.H; p.Hkv = d.Hkv; p.rep = d.H / d.Hkv; p.n_q = d.n_q; p.n_kv = d.n_kv;
+  p.n_pad = l.n_pad;
+  p.q_tiles = l.n_pad / kT;
+  p.items = p.q_tiles * d.H * d.B;      // fewer than 2^31: every item has at least one query row
+  p.kv_tiles = l.kv_tiles; p.splits = l.splits;
+  p.scale = d.scale; p.scale_log2 = d.scale * kLog2e;
+  p.kv_len = a.kv_len;
+  float* lse2 = reinterpret_cast<float*>(ws + l.lse2);
+  float* delta = reinterpret_cast<float*>(ws + l.delta);
+  p.lse2 = lse2; p.delta = delta; p.partial = reinterpret_cast<float*>(ws + l.partial);
+  p.dev_status = a.dev_status;
+  const int tiles = d.B * d.Hkv * l.kv_tiles;      // at most 2^25: a tile has a state of 64 elements
+  MLA_CUDA_TRY(cudaFuncSetAttribute(cross_dq_tc_kernel<D>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, DqShape<D>::kSmem));
+  MLA_CUDA_TRY(cudaFuncSetAttribute(cross_dkv_tc_kernel<D>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, DkvShape<D>::kSmem));
+  MLA_CUDA_TRY(launch_pdl(cross_stats_kernel<D>, dim3(l.n_pad / kStatRows, d.H, d.B), dim3(256), 0, s,
+                          static_cast<const bf16*>(a.out), static_cast<const bf16*>(a.d_out), a.lse,
+                          lse2, delta, d.H, d.n_q, l.n_pad));
+  MLA_CUDA_TRY(launch_pdl(cross_dq_tc_kernel<D>, dim3(std::min(p.items, 148)), dim3(kThreads),
+                          DqShape<D>::kSmem, s, tq, tg, tk, tv, tdq, static_cast<bf16*>(a.d_q), p));
+  MLA_CUDA_TRY(launch_pdl(cross_dkv_tc_kernel<D>, dim3(tiles * l.splits),
+                          dim3(kThreadsKV), DkvShape<D>::kSmem, s, tq, tg, tk, tv, p));
+  MLA_CUDA_TRY(launch_pdl(cross_dkv_reduce_kernel<D>, dim3(tiles * (D / 8)),
+                          dim3(kT), 0, s, static_cast<bf16*>(a.d_k), static_cast<bf16*>(a.d_v), p));
+  return MLA_OK;
+}
+
+}  // namespace
+
+size_t cross_bwd_tc_workspace(const CrossDims& d) { return bwd_layout(d).bytes; }
+
+mla_status cross_bwd_tc(const CrossDims& d, const CrossBwdArgs& a, void* workspace,
+                        cudaStream_t s) {
+  return d.d == 128 ? bwd_impl<128>(d, a, workspace, s) : bwd_impl<64>(d, a, workspace, s);
+}
+
+}  // namespace mla

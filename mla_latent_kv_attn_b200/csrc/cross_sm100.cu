@@ -28,10 +28,7 @@
 // and the CUDA cores in turn (6000 cycles a pair of tiles, against 2048 of products and 4500 as it is).
 // States past a sample's length are masked: their scores become -infinity by selection, and their
 // value rows are overwritten with zeros in shared memory (0 * NaN would reach O).
-#include "cross.h"
-#include "exp2.cuh"
-#include "kernels.h"
-#include "sm100.cuh"
+#include "cross_tc.cuh"
 
 namespace mla {
 
@@ -39,8 +36,8 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kBM = 128;             // query rows of a stream
-constexpr int kBN = 128;             // states of a tile
+constexpr int kBM = kCrossTile;      // query rows of a stream
+constexpr int kBN = kCrossTile;      // states of a tile
 constexpr int kStreamThreads = 256;
 constexpr int kProducerWarp = 16;
 constexpr int kIssuerWarp = 17;      // and 18; warp 17 also allocates TMEM
@@ -48,7 +45,6 @@ constexpr int kStoreWarp = 19;
 constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D_>
 struct FwdShape {
@@ -112,21 +108,6 @@ __device__ __forceinline__ Item item_of(const CrossFwdParams& p, int it) {
   w.len = cross_len(p.kv_len, w.b, p.n_kv);
   w.nt = ceil_div(w.len, kBN);
   return w;
-}
-
-// Zeros rows [from, to) of a tile of kBlocks blocks of 128-byte rows (whatever the swizzle: it
-// permutes within a row), `threads` threads of index t.
-template <int kBlocks>
-__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int to, int t, int threads) {
-  const int n = (to - from) * 8;
-  for (int i = t; i < n; i += threads) {
-#pragma unroll
-    for (int blk = 0; blk < kBlocks; ++blk)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + blk * 128 * 128 +
-                                                                    from * 128 + i * 16),
-                   "r"(0)
-                   : "memory");
-  }
 }
 
 // The largest of 32 scores; those from `valid` on become -infinity.
@@ -502,11 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e)
             v[e] = pack_bf16x2(__uint_as_float(r[8 * k + 2 * e]) * inv_l,
                                __uint_as_float(r[8 * k + 2 * e + 1]) * inv_l);
-          const uint32_t at = stage + (col / 64) * kBlk + row * 128 +
-                              ((((col % 64) / 8 + k) ^ (row & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
-                       "r"(v[2]), "r"(v[3])
-                       : "memory");
+          store_shared16(swizzled_piece(stage + (col / 64) * kBlk, row, (col % 64) / 8 + k), v);
         }
       }
       tc_fence_before();
@@ -524,17 +501,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-}
-
-// Tensor map of [B, n, heads, d] rows with 64-column, `rows`-row boxes, 128-byte swizzle.
-mla_status cross_tmap(CUtensorMap* m, const void* base, int B, int n, int heads, int d, int64_t row,
-                      uint32_t rows) {
-  const uint64_t dims[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(heads),
-                            static_cast<uint64_t>(n), static_cast<uint64_t>(B)};
-  const uint64_t strides[3] = {d * 2ull, static_cast<uint64_t>(row) * 2,
-                               static_cast<uint64_t>(n) * static_cast<uint64_t>(row) * 2};
-  const uint32_t box[4] = {64, 1, rows, 1};
-  return make_tmap_bf16(m, base, 4, dims, strides, box, 128);
 }
 
 template <int D>

@@ -409,15 +409,12 @@ mla_status cross_dims(const mla_cross_config* cfg, int64_t q_row, int64_t k_row,
   return check_row_stride(v_row, kw, int64_t{c.batch} * c.n_kv, c.dtype, "v", &d->v_row);
 }
 
-struct CrossBwdWorkspace {
-  size_t delta_bytes, bytes;
-};
-
-CrossBwdWorkspace cross_bwd_workspace_layout(const mla_cross_config& c) {
-  CrossBwdWorkspace w;
-  w.delta_bytes = (static_cast<size_t>(c.batch) * c.n_heads * c.n_q * sizeof(float) + 255) / 256 * 256;
-  w.bytes = w.delta_bytes;
-  return w;
+// delta of every query row, or what the tensor-core kernels keep.
+size_t cross_bwd_workspace(const CrossDims& d) {
+  const size_t bytes = cross_tc_supported(d)
+                           ? cross_bwd_tc_workspace(d)
+                           : static_cast<size_t>(d.B) * d.H * d.n_q * sizeof(float);
+  return (bytes + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -914,8 +911,8 @@ mla_status mla_cross_attention_fwd(const mla_cross_config* cfg, const void* q, i
 }
 
 size_t mla_cross_attention_bwd_workspace_bytes(const mla_cross_config* cfg) {
-  if (check_cross_cfg(cfg) != MLA_OK) return 0;
-  return cross_bwd_workspace_layout(*cfg).bytes;
+  CrossDims d;
+  return cross_dims(cfg, 0, 0, 0, &d) == MLA_OK ? cross_bwd_workspace(d) : 0;
 }
 
 mla_status mla_cross_attention_bwd(const mla_cross_config* cfg, const void* q, int64_t q_row_stride,
@@ -939,12 +936,13 @@ mla_status mla_cross_attention_bwd(const mla_cross_config* cfg, const void* q, i
   MLA_TRY(check_ptr(d_k, "d_k"));
   MLA_TRY(check_ptr(d_v, "d_v"));
   MLA_TRY(check_ptr(dev_status, "dev_status", false));
-  const CrossBwdWorkspace w = cross_bwd_workspace_layout(*cfg);
-  MLA_TRY(check_scratch(workspace, workspace_bytes, w.bytes));
+  MLA_TRY(check_scratch(workspace, workspace_bytes, cross_bwd_workspace(d)));
   CrossBwdArgs a{};
   a.q = q; a.k = k; a.v = v; a.kv_len = kv_len; a.out = out; a.lse = lse; a.d_out = d_out;
   a.d_q = d_q; a.d_k = d_k; a.d_v = d_v; a.dev_status = dev_status;
-  return cross_bwd_simt(d, a, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cross_tc_supported(d) ? cross_bwd_tc(d, a, workspace, s)
+                               : cross_bwd_simt(d, a, static_cast<float*>(workspace), s);
 }
 
 }  // extern "C"

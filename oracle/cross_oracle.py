@@ -5,6 +5,11 @@ from __future__ import annotations
 import numpy as np
 
 
+# fp32 exponentials below the least normal number become 0, and one from a polynomial whose argument
+# is held at -125 or more becomes 2^-125: a probability may be off by that, whatever its size.  (In
+# the gradients it stands beside factors such as g.v, so even 0 <-> 2^-125 shows in results that
+# should be 1e-41.)
+TINY = 2.0 ** -125
 F32 = 2.0 ** -23     # a step of fp32: a sum of n terms is off by at most n F32 sum |term|
 
 
@@ -35,7 +40,7 @@ def cross_attention(q, k, v, lens, scale, p_rel=0.0):
             e_x = _score_error(qq, kk, scale, x, lse[b, h])
             e_lse[b, h] = (p * e_x).sum(1) + (n + 4) * F32 + 4 * F32 * np.abs(lse[b, h])
             # numerator and denominator: the weights' own errors, and those of the two sums
-            e_p = p * (p_rel + e_x + (n + 4) * F32)
+            e_p = p * (p_rel + e_x + (n + 4) * F32) + TINY
             e_out[b, :, h] = e_p @ np.abs(vv) + e_p.sum(1)[:, None] * np.abs(out[b, :, h])
     return out, lse, e_out, e_lse
 
@@ -74,13 +79,14 @@ def cross_attention_backward(q, k, v, lens, scale, g, p_rel=0.0, o_rel=0.0, ds_r
                 + sums * (a_g * np.abs(out[b, :, h])).sum(1)
             e_dp = sums * (a_g @ a_v.T)
             e_ds = (ds_rel + e_x + 4 * F32) * np.abs(ds) + \
-                scale * p * (e_delta[:, None] + e_dp) * (1 + ds_rel)
+                scale * p * (e_delta[:, None] + e_dp) * (1 + ds_rel) + \
+                scale * TINY * (np.abs(dp - delta) + e_delta[:, None] + e_dp)
             if n == 1:
                 e_ds = np.zeros_like(e_ds)
             e_q[b, :, h] = e_ds @ a_k + (n + 4) * F32 * (np.abs(ds) @ a_k)
             long = (rep * n_q + 4) * F32
             e_k[b, :n, kh] += e_ds.T @ a_q + long * (np.abs(ds).T @ a_q)
-            e_v[b, :n, kh] += (p * (p_rel + e_x)).T @ a_g + long * (p.T @ a_g)
+            e_v[b, :n, kh] += (p * (p_rel + e_x) + TINY).T @ a_g + long * (p.T @ a_g)
     return (d_q, d_k, d_v), (e_q, e_k, e_v)
 
 
