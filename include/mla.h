@@ -503,10 +503,14 @@ mla_status mla_out_proj(const mla_config* cfg, const void* o_lat, const void* w_
  * mla_cache_read_q4: every row's values, cache device T [B, window_frames*tpf, D].
  * mla_attention_fwd_q4, mla_attention_fwd_from_cq_q4: mla_attention_fwd and
  *   mla_attention_fwd_from_cq over such a ring (every other argument, shape and error as there).
- *   They equal those calls on the ring that mla_cache_read_q4 gives, bit for bit.  One pass decodes
- *   the attended slots into the workspace and writes every rotated key; the attention follows.
+ *   One pass decodes the attended slots into the workspace and writes every rotated key; the
+ *   attention follows.  On CUDA cores the result is that of the call on the ring that
+ *   mla_cache_read_q4 gives, bit for bit.  On the tensor cores (whichever kernel_path names them)
+ *   the operands are fp16, which holds the ring's values exactly and rounds the rest to 2^-11 of
+ *   itself: the chunk's latents beyond 65504 are taken as 65504, below 2^-14 to 2^-25.
  *   Workspace: mla_attention_q4_workspace_bytes (0 for a bad configuration), 256-byte aligned; it
- *   holds the attended slots as T values for the length of the call, so one serves every layer.
+ *   holds the attended slots as 16-bit or T values for the length of the call, so one serves every
+ *   layer.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_ALIGNMENT, MLA_ERR_WORKSPACE,
  * MLA_ERR_CUDA.
  * ------------------------------------------------------------------------------------------ */

@@ -31,6 +31,14 @@
 // buffer for the same reason.
 // With DC = 256 O and P leave no room for Q: Q stays in shared memory, there are two S buffers,
 // P(j) is written into S buffer j&1 and QK(j+2) waits for PV(j).
+//
+// kHalf: the same kernel with fp16 operands in place of bf16, for keys and values that fp16 holds
+// exactly or nearly so (the 4-bit ring's, ring_q4.cu).  fp16 has three bits more at the same rate:
+// what rounding the query, the rotated keys and P costs falls by 8 (lse of 64 to 6000 keys within
+// 1e-5 of itself, where bf16 gives up to 1e-4).  Its range is narrower, so a query row is scaled by
+// a power of two that brings its largest element to 2^14 .. 2^15, and the row's scores are scaled
+// back; P stays below 2^8.  The latent output meets W_UV (bf16) as the sum of two bf16 numbers,
+// both from TMEM, instead of one: 12 products more in an epilogue, and no rounding of it.
 #include "exp2.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -110,9 +118,15 @@ struct AttnParams {
 // Pairs (out of every 8) of a full key tile whose exponentials take the FMA-pipe polynomial.
 constexpr int kPolyPairsPer8 = 2;
 
-// p = 2^(s * scale_log2 - m) for one row of a key tile: packed to bf16 pairs in w, returning
+// Pairs of MMA operands: bf16, or fp16 with kHalf.
+template <bool kHalf>
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+  return kHalf ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+}
+
+// p = 2^(s * scale_log2 - m) for one row of a key tile: packed to bf16 (fp16) pairs in w, returning
 // the row sum.  kPoly: some pairs use exp2_poly_pair (full tiles; no masked -inf scores).
-template <bool kPoly>
+template <bool kPoly, bool kHalf>
 __device__ __forceinline__ float softmax_exp_row(const float (&s)[kKeyTile], float scale_log2,
                                                  float m, uint32_t (&w)[kKeyTile / 2]) {
   const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
@@ -129,7 +143,7 @@ __device__ __forceinline__ float softmax_exp_row(const float (&s)[kKeyTile], flo
       p1 = fast_exp2(x1);
     }
     sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(p0, p1));
-    w[i] = pack_bf16x2(p0, p1);
+    w[i] = pack_pair<kHalf>(p0, p1);
   }
   const uint64_t t2 = f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]));
   float l0, l1;
@@ -162,13 +176,77 @@ __device__ __noinline__ void copy_q_row(uint32_t taddr, const bf16* row) {
   }
 }
 
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((e + 127) << 23); }
+
+// The exponent e for which 2^e brings a number with biased exponent `biased` to 2^top .. 2^(top+1),
+// as far as 2^e and 2^-e are normal numbers (a row of zeros or of the least subnormals is not).
+__device__ __forceinline__ int scale_exponent(uint32_t biased, int top) {
+  return min(top + 127 - static_cast<int>(biased), 126);
+}
+
+// A bf16 query row as fp16 pairs, scaled by 2^e so that its largest element lies in 2^14 .. 2^15:
+// to this thread's TMEM lane from column `at` on (zeros past D/2), or with kSmem to row `row` of the
+// Q tile at shared address `at`.  Returns 2^-e.
+template <int DC, int D, int kQWords, bool kSmem>
+__device__ __noinline__ float copy_q_row_f16(uint32_t at, int row, const bf16* src) {
+  const uint4* s4 = reinterpret_cast<const uint4*>(src);
+  uint32_t top = 0;
+  if (src != nullptr) {
+#pragma unroll 4
+    for (int u = 0; u < D / 8; ++u) {
+      const uint4 v = s4[u];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7f80u, (w[k] >> 16) & 0x7f80u));
+    }
+  }
+  const int e = scale_exponent(top >> 7, 14);
+  const float f = pow2(e);
+#pragma unroll 1
+  for (int u = 0; u < kQWords / 4; u += 4) {        // 32 values
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4 v = src != nullptr && u + k < D / 8 ? s4[u + k] : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[4 * k + i] = pack_f16x2(__uint_as_float(x[i] << 16) * f,
+                                  __uint_as_float(x[i] & 0xffff0000u) * f);
+    }
+    if constexpr (kSmem) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int piece = u + k;
+        if (piece >= D / 8) break;
+        uint32_t to;
+        if (piece < DC / 8) {
+          to = at + (piece / 8) * kQBlk + row * 128 + (((piece % 8) ^ (row & 7)) << 4);
+        } else {
+          // the positional block: rows of 32, 64 or 128 bytes, swizzled at that width
+          constexpr int kPieces = (D - DC) / 8;
+          const int r = piece - DC / 8;
+          const int x = kPieces == 8 ? row & 7 : kPieces == 4 ? (row >> 1) & 3 : (row >> 2) & 1;
+          to = at + (DC / 64) * kQBlk + row * (16 * kPieces) + ((r ^ x) << 4);
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w[4 * k]),
+                     "r"(w[4 * k + 1]), "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
+                     : "memory");
+      }
+    } else {
+      tmem_st16(at + 4 * u, w);
+    }
+  }
+  return pow2(-e);
+}
+
 // Fused query heads: one row of Q'_h (fp32, TMEM columns kColO .. kColO+D of this thread's lane)
 // rotated by 3D-RoPE in its last D-DC columns at chunk token n's position, rounded once to
 // bf16 and stored as pairs from column kColS (zeros past D/2) - what the Q' GEMM's epilogue
 // stores.  16 columns at a time: D is a multiple of 16 and DC of 64.
-template <int DC>
+template <int DC, bool kHalf>
 __device__ __forceinline__ void q_piece(uint32_t tlane, int c, const AttnParams& p, int t, int hh,
-                                        int ww, uint32_t* w8) {
+                                        int ww, float f, uint32_t* w8) {
   uint32_t r[16];
   tmem_ld16_wait(tlane + kColO + c, r);
   float v[16];
@@ -179,12 +257,30 @@ __device__ __forceinline__ void q_piece(uint32_t tlane, int c, const AttnParams&
     for (int k = 0; k < 16; k += 2)
       rope_rotate(v[k], v[k + 1], rope_angle(p.rope, (c - DC + k) >> 1, t, hh, ww));
   }
+  if constexpr (kHalf) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) w8[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+    for (int k = 0; k < 16; ++k) v[k] *= f;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w8[k] = pack_pair<kHalf>(v[2 * k], v[2 * k + 1]);
 }
 
-template <int DC, int D, int kQWords>
-__device__ __noinline__ void q_row_from_accumulator(uint32_t tlane, const AttnParams& p, int n) {
+// (kHalf: the row scaled by 2^e with its largest element in 2^13 .. 2^14 - a rotation may add half
+// an exponent; returns 2^-e, else 1.)
+template <int DC, int D, int kQWords, bool kHalf>
+__device__ __noinline__ float q_row_from_accumulator(uint32_t tlane, const AttnParams& p, int n) {
+  int e = 0;
+  if constexpr (kHalf) {
+    uint32_t top = 0;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+      uint32_t r[16];
+      tmem_ld16_wait(tlane + kColO + c, r);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) top = max(top, r[k] & 0x7f800000u);
+    }
+    e = scale_exponent(top >> 23, 13);
+  }
   const int nl = n < p.n_q ? n : 0;
   const int i = nl % p.rope.tpf;
   const int t = p.first_frame + nl / p.rope.tpf, hh = i / p.rope.frame_w, ww = i % p.rope.frame_w;
@@ -193,10 +289,11 @@ __device__ __noinline__ void q_row_from_accumulator(uint32_t tlane, const AttnPa
     uint32_t w[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) w[k] = 0u;
-    if (c < D) q_piece<DC>(tlane, c, p, t, hh, ww, w);
-    if (c + 16 < D) q_piece<DC>(tlane, c + 16, p, t, hh, ww, w + 8);
+    if (c < D) q_piece<DC, kHalf>(tlane, c, p, t, hh, ww, pow2(e), w);
+    if (c + 16 < D) q_piece<DC, kHalf>(tlane, c + 16, p, t, hh, ww, pow2(e), w + 8);
     tmem_st16(tlane + kColS + c / 2, w);
   }
+  return pow2(-e);
 }
 
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag,
@@ -204,7 +301,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   return mbar_wait_or_abort(bar, parity, abort_flag, dev_status);
 }
 
-template <int DC, int DR, bool kFusedQ>
+template <int DC, int DR, bool kFusedQ, bool kHalf>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qr,
                         const __grid_constant__ CUtensorMap tm_cache,
@@ -254,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     abort_sh = 0;
-    mbar_init(smem_u32(&q_full), kQTmem ? kSoftmaxThreads : 1);
+    mbar_init(smem_u32(&q_full), kQTmem || kHalf ? kSoftmaxThreads : 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&kv_full[s]), 1);
       mbar_init(smem_u32(&kv_empty[s]), 1);
@@ -292,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       tma_prefetch_desc(&tm_chunk);
       tma_prefetch_desc(&tm_ws);
-      if constexpr (!kQTmem) {
+      if constexpr (!kQTmem && !kHalf) {
         tma_prefetch_desc(&tm_q);
         const uint32_t qb = smem_u32(&q_full);
         mbar_arrive_expect_tx(qb, kQTile);
@@ -355,8 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // explicit: QK(j) overwrites the S/P buffer that PV(j-2) reads, so it waits for PV(j-2).
     // With Q in TMEM there is one S buffer, which QK(j) takes once the softmax has loaded S(j-1).
     if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(kBM, kBN, 0, 0);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(kBM, kDc, 0, 1);
+      constexpr uint32_t idesc_qk = kHalf ? idesc_f16_f32(kBM, kBN, 0, 0)
+                                          : idesc_bf16_f32(kBM, kBN, 0, 0);
+      constexpr uint32_t idesc_pv = kHalf ? idesc_f16_f32(kBM, kDc, 0, 1)
+                                          : idesc_bf16_f32(kBM, kDc, 0, 1);
       constexpr uint32_t idesc_uv = idesc_bf16_f32(kBM, kDh, 0, 0);
       // Descriptors are built once; an operand at byte offset `off` from a descriptor's start
       // is that descriptor plus off/16 (the start-address field is the low 14 bits and every
@@ -460,12 +559,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t o_c =
                 kQTmem ? smem_desc(sK0 + ((nqc + p.nt + 1) % kStages) * kKTile, 16, 1024, kSwizzle128B)
                        : q_c;
+            if constexpr (kHalf) {
+              // O_lat = hi + lo, both from TMEM
 #pragma unroll
-            for (int blk = 0; blk < kCBlk; ++blk)
+              for (int part = 0; part < 2; ++part)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ss(tmem, o_c + (blk * kQBlkD + 2 * kk), w_c + (blk * kQBlkD + 2 * kk), idesc_uv,
-                       (blk | kk) != 0 ? 1u : 0u);
+                for (int kk = 0; kk < kDc / 16; ++kk)
+                  mma_ts(tmem, tmem + (part == 0 ? kColS : kColO) + 8 * kk,
+                         w_c + ((kk >> 2) * kQBlkD + 2 * (kk & 3)), idesc_uv,
+                         (part | kk) != 0 ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int blk = 0; blk < kCBlk; ++blk)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_ss(tmem, o_c + (blk * kQBlkD + 2 * kk), w_c + (blk * kQBlkD + 2 * kk), idesc_uv,
+                         (blk | kk) != 0 ? 1u : 0u);
+            }
             mma_commit(smem_u32(&epi_done));
           }
         }
@@ -476,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = warp * 32 + lane;                 // TMEM lane and query row in the tile
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     const int n = q0 + row;
+    [[maybe_unused]] float row_scale_log2 = p.scale_log2;     // kHalf: with the row's power of two
     if constexpr (kFusedQ) {
       // this row of Q'_h out of its fp32 accumulator, the positional part rotated at the row's
       // position, into the query's TMEM columns as bf16 pairs
@@ -483,10 +594,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                         p.dev_status));
       if (okq) {
         tc_fence_after();
-        q_row_from_accumulator<DC, Sh::D, Sh::kQWords>(tmem + lane_off, p, n);
+        const float f = q_row_from_accumulator<DC, Sh::D, Sh::kQWords, kHalf>(tmem + lane_off, p, n);
+        if constexpr (kHalf) row_scale_log2 *= f;
       }
       tmem_wait_st();
       tc_fence_before();
+      mbar_arrive(smem_u32(&q_full));
+    } else if constexpr (kHalf) {
+      row_scale_log2 *= copy_q_row_f16<DC, Sh::D, Sh::kQWords, !kQTmem>(
+          kQTmem ? tmem + lane_off + kColS : sQ, row,
+          n < p.n_q ? p.q + ((static_cast<int64_t>(b) * p.n_q + n) * p.H + h) * Sh::D : nullptr);
+      if constexpr (kQTmem) {
+        tmem_wait_st();
+        tc_fence_before();
+      } else {
+        fence_proxy_async_smem();
+      }
       mbar_arrive(smem_u32(&q_full));
     } else if constexpr (kQTmem) {
       // this row of the query tile into TMEM, bf16 pairs from column kColS (zeros past D/2
@@ -535,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m8[u] = fmaxf(a, s[kBN - 8 + u]);
         }
         mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) *
-             p.scale_log2;
+             (kHalf ? row_scale_log2 : p.scale_log2);
       }
       // S(j) is in registers: its TMEM buffer may take the next QK (with P in its own buffer;
       // an aliased P keeps the buffer until PV(j) has read it).  Released after the row max,
@@ -563,8 +686,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // unit or, for a fixed share of the pairs of full tiles, the FMA-pipe polynomial; packed
       // to bf16 pairs; the row sum runs in four packed FADD2 chains.
       uint32_t w[kBN / 2];
-      if (valid == kBN) l_run += softmax_exp_row<true>(s, p.scale_log2, m_run, w);
-      else l_run += softmax_exp_row<false>(s, p.scale_log2, m_run, w);
+      const float sl2 = kHalf ? row_scale_log2 : p.scale_log2;
+      if (valid == kBN) l_run += softmax_exp_row<true, kHalf>(s, sl2, m_run, w);
+      else l_run += softmax_exp_row<false, kHalf>(s, sl2, m_run, w);
       // The P buffer and O are free once PV(j-1) has completed (an aliased P needs only O).
       if (j > 0 && (!kAliasP || rescale)) {
         ok = __all_sync(0xffffffffu,
@@ -624,24 +748,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Q in TMEM, into the K' stage after the one W_UV went to: all stages are free now).
         const uint32_t so = kQTmem ? sK0 + ((nqc + p.nt + 1) % kStages) * kKTile : sQ;
         uint8_t* qsm = smem_raw + (so - smem_u32(smem_raw));
+        if constexpr (kHalf) {
+          // O_lat as hi + lo in bf16 pairs: hi from column kColS (Q or an S buffer, read by now), lo
+          // over the columns of O that have been read
 #pragma unroll 1
-        for (int c = 0; c < kDc; c += 32) {
-          uint32_t r[32];
-          tmem_ld32_wait(tmem + lane_off + kColO + c, r);
-          const int blk = c / 64;
+          for (int c = 0; c < kDc; c += 32) {
+            uint32_t r[32], hi[16], lo[16];
+            tmem_ld32_wait(tmem + lane_off + kColO + c, r);
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {         // four 16-byte chunks of 8 values
-            const int chunk = (c % 64) / 8 + ch;   // chunk index within the 128-byte row
-            uint4 v;
-            v.x = pack_bf16x2(__uint_as_float(r[8 * ch + 0]) * inv_l, __uint_as_float(r[8 * ch + 1]) * inv_l);
-            v.y = pack_bf16x2(__uint_as_float(r[8 * ch + 2]) * inv_l, __uint_as_float(r[8 * ch + 3]) * inv_l);
-            v.z = pack_bf16x2(__uint_as_float(r[8 * ch + 4]) * inv_l, __uint_as_float(r[8 * ch + 5]) * inv_l);
-            v.w = pack_bf16x2(__uint_as_float(r[8 * ch + 6]) * inv_l, __uint_as_float(r[8 * ch + 7]) * inv_l);
-            const int off = blk * kQBlk + row * 128 + ((chunk ^ (row & 7)) * 16);
-            *reinterpret_cast<uint4*>(qsm + off) = v;
+            for (int i = 0; i < 16; ++i) {
+              const float x0 = __uint_as_float(r[2 * i]) * inv_l;
+              const float x1 = __uint_as_float(r[2 * i + 1]) * inv_l;
+              hi[i] = pack_bf16x2(x0, x1);
+              lo[i] = pack_bf16x2(x0 - __uint_as_float(hi[i] << 16),
+                                  x1 - __uint_as_float(hi[i] & 0xffff0000u));
+            }
+            tmem_st16(tmem + lane_off + kColS + c / 2, hi);
+            tmem_st16(tmem + lane_off + kColO + c / 2, lo);
           }
+          tmem_wait_st();
+          tc_fence_before();
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kDc; c += 32) {
+            uint32_t r[32];
+            tmem_ld32_wait(tmem + lane_off + kColO + c, r);
+            const int blk = c / 64;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {         // four 16-byte chunks of 8 values
+              const int chunk = (c % 64) / 8 + ch;   // chunk index within the 128-byte row
+              uint4 v;
+              v.x = pack_bf16x2(__uint_as_float(r[8 * ch + 0]) * inv_l, __uint_as_float(r[8 * ch + 1]) * inv_l);
+              v.y = pack_bf16x2(__uint_as_float(r[8 * ch + 2]) * inv_l, __uint_as_float(r[8 * ch + 3]) * inv_l);
+              v.z = pack_bf16x2(__uint_as_float(r[8 * ch + 4]) * inv_l, __uint_as_float(r[8 * ch + 5]) * inv_l);
+              v.w = pack_bf16x2(__uint_as_float(r[8 * ch + 6]) * inv_l, __uint_as_float(r[8 * ch + 7]) * inv_l);
+              const int off = blk * kQBlk + row * 128 + ((chunk ^ (row & 7)) * 16);
+              *reinterpret_cast<uint4*>(qsm + off) = v;
+            }
+          }
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
         mbar_arrive(smem_u32(&olat_full));
         ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&epi_done), 0, abort_flag, p.dev_status));
         if (ok) {
@@ -683,11 +829,13 @@ struct FusedQ {
   int first_frame;
 };
 
-template <int DC, int DR, bool kFusedQ>
+// kHalf: a.cache, a.chunk_lat and a.ws hold fp16 values, the latents DC wide.
+template <int DC, int DR, bool kFusedQ, bool kHalf>
 mla_status attention_tc_impl(const Dims& d, const AttnArgs& a, int n_valid, cudaStream_t s,
                              const FusedQ* fq = nullptr) {
   using Sh = AttnShape<DC, DR>;
   constexpr int kD = Sh::D;
+  constexpr int kRow = kHalf ? DC : kD;      // latents per row of the ring and of the chunk
   const KeyWorkspace kw = key_workspace_layout(d, n_valid);
   CUtensorMap tq, tqr, tcache, tchunk, tws, twuv, tcq, twq;
   mla_status st;
@@ -718,16 +866,16 @@ mla_status attention_tc_impl(const Dims& d, const AttnArgs& a, int n_valid, cuda
     twq = tq;
   }
   {
-    const uint64_t dims[3] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(d.n_q),
+    const uint64_t dims[3] = {static_cast<uint64_t>(kRow), static_cast<uint64_t>(d.n_q),
                               static_cast<uint64_t>(d.B)};
-    const uint64_t strides[2] = {kD * 2ull, static_cast<uint64_t>(d.n_q) * kD * 2};
+    const uint64_t strides[2] = {kRow * 2ull, static_cast<uint64_t>(d.n_q) * kRow * 2};
     const uint32_t box[3] = {64, kBN, 1};
     if ((st = make_tmap_bf16(&tchunk, a.chunk_lat, 3, dims, strides, box, 128)) != MLA_OK) return st;
   }
   if (kw.nc > 0) {
-    const uint64_t dims[3] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(kw.nc),
+    const uint64_t dims[3] = {static_cast<uint64_t>(kRow), static_cast<uint64_t>(kw.nc),
                               static_cast<uint64_t>(d.B)};
-    const uint64_t strides[2] = {kD * 2ull, static_cast<uint64_t>(d.W) * d.tpf * kD * 2};
+    const uint64_t strides[2] = {kRow * 2ull, static_cast<uint64_t>(d.W) * d.tpf * kRow * 2};
     const uint32_t box[3] = {64, kBN, 1};
     if ((st = make_tmap_bf16(&tcache, a.cache, 3, dims, strides, box, 128)) != MLA_OK) return st;
   } else {
@@ -760,10 +908,10 @@ mla_status attention_tc_impl(const Dims& d, const AttnArgs& a, int n_valid, cuda
   p.nqc = kFusedQ ? d.d_cq / 64 : 0;
   p.first_frame = kFusedQ ? fq->first_frame : 0;
   p.rope = rope_geom(d);
-  MLA_CUDA_TRY(cudaFuncSetAttribute(attention_tc_kernel<DC, DR, kFusedQ>,
+  MLA_CUDA_TRY(cudaFuncSetAttribute(attention_tc_kernel<DC, DR, kFusedQ, kHalf>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem));
   dim3 grid(ceil_div(d.n_q, kBM), d.H, d.B);
-  MLA_CUDA_TRY(launch_pdl(attention_tc_kernel<DC, DR, kFusedQ>, grid, dim3(kThreads), Sh::kSmem,
+  MLA_CUDA_TRY(launch_pdl(attention_tc_kernel<DC, DR, kFusedQ, kHalf>, grid, dim3(kThreads), Sh::kSmem,
                           s, tq, tqr, tcache, tchunk, tws, twuv, tcq, twq, p));
   MLA_LAUNCH_CHECK("attention_tc");
   return MLA_OK;
@@ -776,9 +924,12 @@ bool tc_attention_supported(const Dims& d, bool has_w_uv) {
          (d.d_rope == 16 || d.d_rope == 32 || d.d_rope == 64) && (!has_w_uv || d.d_head == kDh);
 }
 
-mla_status attention_tc(const Dims& d, const AttnArgs& a, int n_valid, cudaStream_t s) {
+namespace {
+
+template <bool kHalf>
+mla_status attention_tc_typed(const Dims& d, const AttnArgs& a, int n_valid, cudaStream_t s) {
 #define MLA_ATTN_CASE(DC, DR) \
-  if (d.d_c == DC && d.d_rope == DR) return attention_tc_impl<DC, DR, false>(d, a, n_valid, s);
+  if (d.d_c == DC && d.d_rope == DR) return attention_tc_impl<DC, DR, false, kHalf>(d, a, n_valid, s);
   MLA_ATTN_CASE(128, 16) MLA_ATTN_CASE(128, 32) MLA_ATTN_CASE(128, 64)
   MLA_ATTN_CASE(192, 16) MLA_ATTN_CASE(192, 32) MLA_ATTN_CASE(192, 64)
   MLA_ATTN_CASE(256, 16) MLA_ATTN_CASE(256, 32) MLA_ATTN_CASE(256, 64)
@@ -787,21 +938,48 @@ mla_status attention_tc(const Dims& d, const AttnArgs& a, int n_valid, cudaStrea
            d.d_rope);
 }
 
+}  // namespace
+
+mla_status attention_tc(const Dims& d, const AttnArgs& a, int n_valid, cudaStream_t s) {
+  return attention_tc_typed<false>(d, a, n_valid, s);
+}
+
+mla_status attention_tc_f16(const Dims& d, const AttnArgs& a, int n_valid, cudaStream_t s) {
+  return attention_tc_typed<true>(d, a, n_valid, s);
+}
+
 bool tc_attention_fused_q_supported(const Dims& d, bool has_w_uv) {
   return tc_attention_supported(d, has_w_uv) && d.d_c <= 192 && d.d_c + d.d_rope <= 256 &&
          d.d_cq % 64 == 0 && d.d_cq > 0;
 }
 
-mla_status attention_tc_fused_q(const Dims& d, const AttnArgs& a, int n_valid, const void* c_q,
-                                const void* w_qcat, int first_frame, cudaStream_t s) {
+namespace {
+
+template <bool kHalf>
+mla_status attention_tc_fused_q_typed(const Dims& d, const AttnArgs& a, int n_valid,
+                                      const void* c_q, const void* w_qcat, int first_frame,
+                                      cudaStream_t s) {
   const FusedQ fq{c_q, w_qcat, first_frame};
 #define MLA_ATTN_FQ_CASE(DC, DR) \
-  if (d.d_c == DC && d.d_rope == DR) return attention_tc_impl<DC, DR, true>(d, a, n_valid, s, &fq);
+  if (d.d_c == DC && d.d_rope == DR) \
+    return attention_tc_impl<DC, DR, true, kHalf>(d, a, n_valid, s, &fq);
   MLA_ATTN_FQ_CASE(128, 16) MLA_ATTN_FQ_CASE(128, 32) MLA_ATTN_FQ_CASE(128, 64)
   MLA_ATTN_FQ_CASE(192, 16) MLA_ATTN_FQ_CASE(192, 32) MLA_ATTN_FQ_CASE(192, 64)
 #undef MLA_ATTN_FQ_CASE
   MLA_FAIL(MLA_ERR_UNSUPPORTED, "no fused-query attention kernel for d_c %d, d_rope %d", d.d_c,
            d.d_rope);
+}
+
+}  // namespace
+
+mla_status attention_tc_fused_q(const Dims& d, const AttnArgs& a, int n_valid, const void* c_q,
+                                const void* w_qcat, int first_frame, cudaStream_t s) {
+  return attention_tc_fused_q_typed<false>(d, a, n_valid, c_q, w_qcat, first_frame, s);
+}
+
+mla_status attention_tc_fused_q_f16(const Dims& d, const AttnArgs& a, int n_valid, const void* c_q,
+                                    const void* w_qcat, int first_frame, cudaStream_t s) {
+  return attention_tc_fused_q_typed<true>(d, a, n_valid, c_q, w_qcat, first_frame, s);
 }
 
 }  // namespace mla

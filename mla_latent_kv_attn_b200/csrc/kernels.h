@@ -170,6 +170,11 @@ mla_status attention_tc(const Dims& d, const AttnArgs& a, int n_valid, cudaStrea
 bool tc_attention_fused_q_supported(const Dims& d, bool has_w_uv);
 mla_status attention_tc_fused_q(const Dims& d, const AttnArgs& a, int n_valid, const void* c_q,
                                 const void* w_qcat, int first_frame, cudaStream_t s);
+// The same two with fp16 keys and values: a.cache [B, n_valid * tpf, d_c], a.chunk_lat
+// [B, n_q, d_c] and a.ws (rotated keys) hold fp16; d.W = n_valid.
+mla_status attention_tc_f16(const Dims& d, const AttnArgs& a, int n_valid, cudaStream_t s);
+mla_status attention_tc_fused_q_f16(const Dims& d, const AttnArgs& a, int n_valid, const void* c_q,
+                                    const void* w_qcat, int first_frame, cudaStream_t s);
 // CTA-pair tensor-core attention (attention_pair_sm100.cu): pairs of heads share each key tile.
 bool tc_attention_pair_supported(const Dims& d, bool has_w_uv);
 mla_status attention_tc_pair(const Dims& d, const AttnArgs& a, int n_valid, cudaStream_t s);

@@ -311,6 +311,11 @@ mla_status check_q4(const Dims& d, const void* codes, const void* scales) {
   return check_ptr(scales, "scales");
 }
 
+// Whether the attention over the 4-bit ring runs on the tensor cores, which read it as fp16.
+bool q4_f16(const Dims& d, bool has_w_uv) {
+  return use_tc(d) && tc_attention_supported(d, has_w_uv);
+}
+
 // Shared body of the attention entry points over the 4-bit ring: checks, the pass that decodes the
 // ring's content and writes every rotated key, and the attention kernel over its result.
 mla_status attention_q4_entry(const mla_config* cfg, const void* q, const void* c_q,
@@ -343,20 +348,24 @@ mla_status attention_q4_entry(const mla_config* cfg, const void* q, const void* 
   MLA_TRY(check_ptr(w_uv, "w_uv", false));
   MLA_TRY(check_ptr(lse, "lse", false));
   MLA_TRY(check_ptr(dev_status, "dev_status", false));
-  const Q4Workspace w = q4_workspace_layout(d, n_valid_frames);
+  const bool f16 = q4_f16(d, w_uv != nullptr);
+  const Q4Workspace w = q4_workspace_layout(d, n_valid_frames, f16);
   MLA_TRY(check_scratch(workspace, workspace_bytes, w.bytes));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  void* ring = static_cast<char*>(workspace) + w.key_bytes;
-  MLA_TRY(q4_prepare(d, codes, scales, chunk_lat, slot_frame, n_valid_frames, first_frame, ring,
-                     workspace, dev_status, s));
+  MLA_TRY(q4_prepare(d, codes, scales, chunk_lat, slot_frame, n_valid_frames, first_frame, workspace,
+                     f16, dev_status, s));
   // the decoded rows of a sample follow one another: a ring of n_valid_frames slots
   Dims dr = d;
   dr.W = n_valid_frames;
+  char* ring = static_cast<char*>(workspace) + w.key_bytes;
   AttnArgs a{};
-  a.q = q; a.chunk_lat = chunk_lat; a.cache = ring; a.ws = workspace; a.w_uv = w_uv;
-  a.out = out; a.lse = lse; a.dev_status = dev_status;
-  if (from_cq) return attention_tc_fused_q(dr, a, n_valid_frames, c_q, w_qcat, first_frame, s);
-  return attention_dispatch(dr, a, n_valid_frames, s);
+  a.q = q; a.cache = ring; a.ws = workspace; a.w_uv = w_uv; a.out = out; a.lse = lse;
+  a.chunk_lat = f16 ? ring + w.ring_bytes : chunk_lat;
+  a.dev_status = dev_status;
+  if (from_cq)
+    return attention_tc_fused_q_f16(dr, a, n_valid_frames, c_q, w_qcat, first_frame, s);
+  return f16 ? attention_tc_f16(dr, a, n_valid_frames, s)
+             : attention_dispatch(dr, a, n_valid_frames, s);
 }
 
 // ---- cross attention to an encoder's states ---------------------------------------------------
@@ -855,7 +864,9 @@ size_t mla_attention_q4_workspace_bytes(const mla_config* cfg, int32_t n_valid_f
   if (check_cfg(cfg) != MLA_OK) return 0;
   const Dims d = dims_of(*cfg);
   if (n_valid_frames < 0 || n_valid_frames > d.W) return 0;
-  return q4_workspace_layout(d, n_valid_frames).bytes;
+  // (whether the tensor cores take a call may depend on its w_uv)
+  return std::max(q4_workspace_layout(d, n_valid_frames, q4_f16(d, false)).bytes,
+                  q4_workspace_layout(d, n_valid_frames, q4_f16(d, true)).bytes);
 }
 
 mla_status mla_attention_fwd_q4(const mla_config* cfg, const void* q, const void* chunk_lat,

@@ -8,13 +8,18 @@
 //   encode: s = the smallest scale >= max|x| / 7, c = rint(x / s), so that |x - c s| <= s / 2
 //   (a group beyond 7 times the largest scale saturates; a NaN is stored as 0).
 // Why this scale: c has 3 significant bits and s has 4, so c s has at most 7 and is exact in bf16
-// (8 bits).  The attention kernels then read the very values the ring stands for, and the only
-// loss is that of the codes.  Groups of 16 with a scale byte cost the same as groups of 32 with a
+// (8 bits) and in fp16 (11 bits; the least value, 2^-20, is a multiple of fp16's least step 2^-24,
+// the largest, 26880, is below its limit).  The attention kernels then read the very values the
+// ring stands for, and the only loss is that of the codes.  The tensor-core attention reads them as
+// fp16, whose three bits more make the query's, the rotated keys' and P's rounding 8 times
+// smaller.  Groups of 16 with a scale byte cost the same as groups of 32 with a
 // 16-bit scale and follow the values' range twice as closely.
 //
 // The bits work out without a table: a float's exponent and top three mantissa bits, rounded up,
 // minus a bias are the scale byte.  All three passes are bound by memory, or by latency where they
 // move a few megabytes: one thread per group, 16- and 8-byte accesses, no shared memory.
+#include <cuda_fp16.h>
+
 #include "kernels.h"
 #include "ring_q4.h"
 
@@ -48,13 +53,27 @@ __device__ __forceinline__ void load16(const T* p, float (&x)[kQ4Group]) {
   for (int i = 0; i < kQ4Group; ++i) x[i] = Elem<T>::to_f(t[i]);
 }
 
-template <typename T>
-__device__ __forceinline__ void store16(T* p, const float (&x)[kQ4Group]) {
-  constexpr int kPieces = kQ4Group * sizeof(T) / 16;
+// Values to U: T itself, or fp16 with what lies past its range held at its limits (only a chunk
+// latent can; the ring itself ends at 26880).
+template <typename U>
+struct To {
+  static __device__ __forceinline__ U from(float v) { return Elem<U>::from_f(v); }
+};
+template <>
+struct To<__half> {
+  static __device__ __forceinline__ __half from(float v) {
+    if (isfinite(v)) v = fminf(fmaxf(v, -65504.f), 65504.f);
+    return __float2half_rn(v);
+  }
+};
+
+template <typename U>
+__device__ __forceinline__ void store16(U* p, const float (&x)[kQ4Group]) {
+  constexpr int kPieces = kQ4Group * sizeof(U) / 16;
   uint4 raw[kPieces];
-  T* t = reinterpret_cast<T*>(raw);
+  U* t = reinterpret_cast<U*>(raw);
 #pragma unroll
-  for (int i = 0; i < kQ4Group; ++i) t[i] = Elem<T>::from_f(x[i]);
+  for (int i = 0; i < kQ4Group; ++i) t[i] = To<U>::from(x[i]);
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) reinterpret_cast<uint4*>(p)[i] = raw[i];
 }
@@ -126,38 +145,46 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// What an attention call over the 4-bit ring needs beside the chunk, in one launch and one thread
-// per 16 values:
-//   e <  n_content: content group of ring row r -> ring[b, r, :] (the positional columns of these
-//                   rows are not written; the attention takes positional keys from ws)
-//   e >= n_content: 16 positional values of key-workspace row r: ring slot r decoded, or chunk
-//                   token r - nc_pad, rotated at its position and rounded once; zeros in the
-//                   padding rows (the layout of key_workspace_layout)
+// What an attention call over the 4-bit ring reads, in one launch and one thread per 16 values:
+//   e < n_ring               content group of ring row r -> ring[b, r, :] (rows ring_width wide; the
+//                            attention takes positional keys from ws)
+//   e < n_ring + n_chunk     content group of chunk row r -> chunk[b, r, :]  (fp16 only)
+//   else                     16 positional values of key-workspace row r: ring slot r decoded, or
+//                            chunk token r - nc_pad, rotated at its position and rounded once;
+//                            zeros in the padding rows (the layout of key_workspace_layout)
 // The content is decoded once per call and not inside the attention kernel: there every CTA (one
 // per head and 128 query rows, 444 in the Wan preset's call) reads the whole ring, so it would
 // decode it 444 times over, on the threads that the softmax already keeps busy.
-template <typename T>
+template <typename T, typename U>
 __global__ void __launch_bounds__(kThreads)
     q4_prepare_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                       const T* __restrict__ chunk_lat, const int32_t* __restrict__ slot_frame,
-                      T* __restrict__ ring, T* __restrict__ ws, int B, int W, int D, int d_c,
-                      int n_q, int nc, int nc_pad, int rows_ws, int first_frame, RopeGeom geom,
-                      int32_t* dev_status) {
+                      U* __restrict__ ring, U* __restrict__ chunk, U* __restrict__ ws, int B, int W,
+                      int D, int d_c, int ring_width, int n_q, int nc, int nc_pad, int rows_ws,
+                      int first_frame, RopeGeom geom, int32_t* dev_status) {
   grid_dep_wait();
   grid_dep_launch();
   const int groups = D / kQ4Group, cg = d_c / kQ4Group, rg = groups - cg;
   const int64_t ring_rows = static_cast<int64_t>(W) * geom.tpf;
-  const int64_t n_content = static_cast<int64_t>(B) * nc * cg;
+  const int64_t n_ring = static_cast<int64_t>(B) * nc * cg;
+  const int64_t n_content = n_ring + (chunk != nullptr ? static_cast<int64_t>(B) * n_q * cg : 0);
   const int64_t total = n_content + static_cast<int64_t>(B) * rows_ws * rg;
   for (int64_t e = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; e < total;
        e += static_cast<int64_t>(gridDim.x) * kThreads) {
     float x[kQ4Group];
-    if (e < n_content) {
+    if (e < n_ring) {
       const int g = static_cast<int>(e % cg);
       const int64_t br = e / cg;
       const int64_t src = ((br / nc) * ring_rows + br % nc) * groups + g;
       decode16(reinterpret_cast<const uint2*>(codes)[src], scales[src], x);
-      store16(ring + br * D + g * kQ4Group, x);
+      store16(ring + br * ring_width + g * kQ4Group, x);
+      continue;
+    }
+    if (e < n_content) {
+      const int g = static_cast<int>((e - n_ring) % cg);
+      const int64_t br = (e - n_ring) / cg;
+      load16(chunk_lat + br * D + g * kQ4Group, x);
+      store16(chunk + br * d_c + g * kQ4Group, x);
       continue;
     }
     const int64_t p = e - n_content;
@@ -222,33 +249,52 @@ mla_status q4_read(const Dims& d, const uint8_t* codes, const uint8_t* scales, i
   return MLA_OK;
 }
 
-mla_status q4_prepare(const Dims& d, const uint8_t* codes, const uint8_t* scales,
-                      const void* chunk_lat, const int32_t* slot_frame, int n_valid,
-                      int first_frame, void* ring, void* ws, int32_t* dev_status, cudaStream_t s) {
+namespace {
+
+template <typename T, typename U>
+mla_status prepare(const Dims& d, const uint8_t* codes, const uint8_t* scales,
+                   const void* chunk_lat, const int32_t* slot_frame, int n_valid, int first_frame,
+                   void* workspace, bool f16, int32_t* dev_status, cudaStream_t s) {
   const KeyWorkspace kw = key_workspace_layout(d, n_valid);
-  const int64_t total = static_cast<int64_t>(d.B) * kw.nc * (d.d_c / kQ4Group) +
-                        static_cast<int64_t>(d.B) * kw.rows * (d.d_rope / kQ4Group);
-  const dim3 grid(blocks_for(total));
-  const RopeGeom g = rope_geom(d);
-  if (d.dtype == MLA_FP32)
-    MLA_CUDA_TRY(launch_pdl(q4_prepare_kernel<float>, grid, dim3(kThreads), 0, s, codes, scales,
-                            static_cast<const float*>(chunk_lat), slot_frame,
-                            static_cast<float*>(ring), static_cast<float*>(ws), d.B, d.W, d.D,
-                            d.d_c, d.n_q, kw.nc, kw.nc_pad, kw.rows, first_frame, g, dev_status));
-  else
-    MLA_CUDA_TRY(launch_pdl(q4_prepare_kernel<bf16>, grid, dim3(kThreads), 0, s, codes, scales,
-                            static_cast<const bf16*>(chunk_lat), slot_frame,
-                            static_cast<bf16*>(ring), static_cast<bf16*>(ws), d.B, d.W, d.D,
-                            d.d_c, d.n_q, kw.nc, kw.nc_pad, kw.rows, first_frame, g, dev_status));
+  const Q4Workspace w = q4_workspace_layout(d, n_valid, f16);
+  char* base = static_cast<char*>(workspace);
+  const int64_t rows = static_cast<int64_t>(kw.nc) + (f16 ? d.n_q : 0);
+  const int64_t total = d.B * (rows * (d.d_c / kQ4Group) +
+                               static_cast<int64_t>(kw.rows) * (d.d_rope / kQ4Group));
+  MLA_CUDA_TRY(launch_pdl(
+      q4_prepare_kernel<T, U>, dim3(blocks_for(total)), dim3(kThreads), 0, s, codes, scales,
+      static_cast<const T*>(chunk_lat), slot_frame, reinterpret_cast<U*>(base + w.key_bytes),
+      f16 ? reinterpret_cast<U*>(base + w.key_bytes + w.ring_bytes) : static_cast<U*>(nullptr),
+      reinterpret_cast<U*>(base), d.B, d.W, d.D, d.d_c, f16 ? d.d_c : d.D, d.n_q, kw.nc, kw.nc_pad,
+      kw.rows, first_frame, rope_geom(d), dev_status));
   return MLA_OK;
 }
 
-Q4Workspace q4_workspace_layout(const Dims& d, int n_valid) {
+}  // namespace
+
+mla_status q4_prepare(const Dims& d, const uint8_t* codes, const uint8_t* scales,
+                      const void* chunk_lat, const int32_t* slot_frame, int n_valid,
+                      int first_frame, void* workspace, bool f16, int32_t* dev_status,
+                      cudaStream_t s) {
+  if (f16)
+    return prepare<bf16, __half>(d, codes, scales, chunk_lat, slot_frame, n_valid, first_frame,
+                                 workspace, true, dev_status, s);
+  if (d.dtype == MLA_FP32)
+    return prepare<float, float>(d, codes, scales, chunk_lat, slot_frame, n_valid, first_frame,
+                                 workspace, false, dev_status, s);
+  return prepare<bf16, bf16>(d, codes, scales, chunk_lat, slot_frame, n_valid, first_frame,
+                             workspace, false, dev_status, s);
+}
+
+Q4Workspace q4_workspace_layout(const Dims& d, int n_valid, bool f16) {
   const KeyWorkspace kw = key_workspace_layout(d, n_valid);
+  const auto round256 = [](size_t n) { return (n + 255) / 256 * 256; };
   Q4Workspace w;
-  w.key_bytes = (kw.bytes + 255) / 256 * 256;
-  w.ring_bytes = static_cast<size_t>(d.B) * kw.nc * d.D * dtype_size(d.dtype);
-  w.bytes = w.key_bytes + w.ring_bytes;
+  w.key_bytes = round256(kw.bytes);
+  w.ring_bytes = round256(static_cast<size_t>(d.B) * kw.nc *
+                          (f16 ? d.d_c * sizeof(__half) : d.D * dtype_size(d.dtype)));
+  w.chunk_bytes = f16 ? round256(static_cast<size_t>(d.B) * d.n_q * d.d_c * sizeof(__half)) : 0;
+  w.bytes = w.key_bytes + w.ring_bytes + w.chunk_bytes;
   return w;
 }
 

@@ -116,3 +116,35 @@ def q4_decode(codes, scales):
     codes = np.asarray(codes, dtype=np.int64)
     c = np.stack([codes % 16, codes // 16], -1).reshape(*codes.shape[:-1], -1) - 8
     return c * np.repeat(q4_scale(scales), Q4_GROUP, axis=-1)
+
+
+def latent_attention(q, c, k_r, w_uv, scale, e_q, e_k, p_rel, p_abs):
+    """One sample's attention of q [n_q, H, D] to content latents c [n_k, d_c] and rotated keys k_r
+    [n_k, d_rope] (both unrounded) with w_uv [H, d_head, d_c]: out [n_q, H, d_head], lse [H, n_q],
+    and bounds on their errors when the queries are off by e_q [n_q, H, D], the rotated keys by e_k
+    of themselves (e_k [n_k, d_rope]), the exponentials by p_rel of themselves and p_abs of a row's
+    largest, sums are fp32 and the latent output is held in 16 bits or more (before out is
+    rounded)."""
+    n_q, H, D = q.shape
+    d_c, n = c.shape[1], c.shape[0]
+    keys = np.concatenate([c, k_r], axis=1)
+    e_keys = np.concatenate([np.zeros_like(c), e_k], axis=1)
+    out, e_out = np.zeros((2, n_q, H, w_uv.shape[1]))
+    lse, e_lse = np.zeros((2, H, n_q))
+    for h in range(H):
+        x = scale * q[:, h] @ keys.T
+        m = x.max(1)
+        lse[h] = m + np.log(np.exp(x - m[:, None]).sum(1))
+        p = np.exp(x - lse[h][:, None])
+        e_x = scale * (e_q[:, h] @ (np.abs(keys) + e_keys).T + np.abs(q[:, h]) @ e_keys.T) + \
+            _score_error(q[:, h], keys, scale, x, lse[h])
+        # the row sum takes the unrounded exponentials: p_rel is rounding and polynomial together
+        e_lse[h] = (p * e_x).sum(1) + (p * e_x ** 2).sum(1) + 1.1e-4 + (n + 4) * F32 * \
+            (1 + np.abs(lse[h]))
+        e_p = p * (np.exp(e_x) * (1 + p_rel + (n + 4) * F32) - 1) + p_abs
+        lat = p @ c
+        e_lat = e_p @ np.abs(c) + e_p.sum(1)[:, None] * np.abs(lat) + 2.0 ** -16 * np.abs(lat)
+        out[:, h] = lat @ w_uv[h].T
+        e_out[:, h] = e_lat @ np.abs(w_uv[h]).T + \
+            (d_c + 4) * F32 * (np.abs(lat) @ np.abs(w_uv[h]).T)
+    return out, lse, e_out, e_lse

@@ -152,7 +152,10 @@ def test_q4_refusals_without_a_device():
     args = [None] * 6 + [0, 0] + [None] * 4 + [0, None, None]
     assert lib.mla_attention_fwd_from_cq_q4(ctypes.byref(wide), *args) == _lib.MLA_ERR_UNSUPPORTED
     assert api.mla_attention_q4_workspace_bytes(c, 7) == 0
-    # the rotated keys as for a bf16 ring, and the attended slots as bf16 values
-    tpf, D = 1560, 224
-    keys = api.mla_attention_workspace_bytes(c, 6)
-    assert api.mla_attention_q4_workspace_bytes(c, 6) == -(-keys // 256) * 256 + 6 * tpf * D * 2
+    # the rotated keys as for a bf16 ring, and the contents of slots and chunk in 16 bits
+    tpf, D, d_c = 1560, 224, 192
+    keys = -(-api.mla_attention_workspace_bytes(c, 6) // 256) * 256
+    assert api.mla_attention_q4_workspace_bytes(c, 6) == keys + (6 + 3) * tpf * d_c * 2
+    # CUDA cores: the slots' values beside the caller's chunk
+    simt = api.make_config(inputs.CONFIGS[1], kernel_path=api.MLA_PATH_SIMT)
+    assert api.mla_attention_q4_workspace_bytes(simt, 6) == keys + 6 * tpf * D * 2

@@ -1,6 +1,6 @@
 """The latent ring held in 4 bits on the GPU: codes, scales and values bit for bit against the
-definition; attention over it bit for bit against the same call on the ring's values, and those
-values' rollout against the float64 oracle."""
+definition; attention over it against the float64 definition on the ring's values, element by
+element within bounds derived from the roundings made, and a rollout against the oracle."""
 import dataclasses
 
 import numpy as np
@@ -93,38 +93,103 @@ def _query(c, seed):
     return q.to(api.torch_dtype(c)), w_uv.to(api.torch_dtype(c))
 
 
+# The tensor-core attention over the 4-bit ring rounds its operands to fp16: P and the rotated keys
+# by 2^-11 of themselves (P also by half of fp16's least step, beside a largest value of 1 or more),
+# a formed query likewise; sines and cosines of these small angles are off by 2^-20; an exponential
+# may come from a polynomial that is off by 1e-4.
+F16 = 2.0 ** -11
+
+
+def _reference(c, cfg, values, slots, lat, q, e_q, w_uv, first, n_valid):
+    """out [B, n_q, H, d_head], lse, and the bounds on their errors, from the ring's values."""
+    d = oracle.dims_from(cfg)
+    res = []
+    for b in range(cfg.batch):
+        nc = n_valid * cfg.tokens_per_frame
+        pos = np.concatenate([oracle.token_positions([int(t) for t in slots[b][:n_valid]], d),
+                              oracle.token_positions(range(first, first + cfg.chunk_frames), d)]
+                             ) if n_valid else oracle.token_positions(
+                                 range(first, first + cfg.chunk_frames), d)
+        rows = np.concatenate([values[b][:nc], lat[b]])
+        raw = rows[:, cfg.d_c:]
+        k_r = oracle.rope3d(raw, pos, d)
+        size = np.abs(raw)[:, 0::2] + np.abs(raw)[:, 1::2]        # of a pair: bounds |rotated|
+        e_k = F16 * np.abs(k_r) + 2.0 ** -20 * np.repeat(size, 2, axis=1) + 2.0 ** -25
+        res.append(oracle.latent_attention(q[b], rows[:, :cfg.d_c], k_r, w_uv, cfg.softmax_scale,
+                                           e_q[b], e_k, F16 + 1.1e-4, 2.0 ** -25))
+    return [np.stack(x) for x in zip(*res)]
+
+
+def _within(got, want, bound, r):
+    err = np.abs(to_np(got) - want)
+    limit = bound * (1 + r) + r * np.abs(want)
+    assert np.isfinite(to_np(got)).all()
+    assert (err <= limit).all(), float((err / limit).max())
+    return err
+
+
 @pytest.mark.parametrize("chunks", [0, 1, 5])
-@pytest.mark.parametrize("fuse_uv", [True, False])
-@pytest.mark.parametrize("path,d_c,d_rope", [("tc", 192, 32), ("tc", 128, 16), ("tc", 256, 64),
-                                             ("pair", 192, 32), ("simt", 192, 32)])
-def test_attention_equals_the_call_on_the_rings_values(path, d_c, d_rope, fuse_uv, chunks):
+@pytest.mark.parametrize("path,d_c,d_rope", [("tc", 192, 32), ("tc", 128, 16), ("tc", 192, 64),
+                                             ("tc", 256, 64), ("tc", 256, 32), ("tc", 256, 16),
+                                             ("pair", 192, 32)])
+def test_attention_matches_the_definition(path, d_c, d_rope, chunks):
     cfg = inputs.with_latent_shape(SMALL, d_c, d_rope)
     c, q4, plain = _filled(cfg, PATHS[path], chunks)
     first, n_valid = rollout.chunk_schedule(cfg.chunk_frames, cfg.window_frames, chunks)
     lat, (q, w_uv) = _chunk(c, 100), _query(c, 101)
-    a, b = rollout.ChunkBuffers(c), rollout.ChunkBuffers(c, q4=True)
+    b = rollout.ChunkBuffers(c, q4=True)
     b.workspace.fill_(0xFF)                                # contents on entry must not matter
-    outs = []
-    for buf in (a, b):
-        out = buf.o if fuse_uv else buf.o_lat
-        w = w_uv if fuse_uv else None
-        if buf is a:
-            api.mla_attention_fwd(c, q, lat, plain.cache, plain.slot_frame, n_valid, first, w, out,
-                                  buf.lse, buf.workspace, buf.dev_status)
-        else:
-            need = max(api.mla_attention_q4_workspace_bytes(c, n_valid), 256)
-            api.mla_attention_fwd_q4(c, q, lat, q4.codes, q4.scales, q4.slot_frame, n_valid, first,
-                                     w, out, buf.lse, buf.workspace[:need], buf.dev_status)
-            assert (buf.workspace[need:] == 0xFF).all()
-        outs.append((out, buf.lse))
+    need = max(api.mla_attention_q4_workspace_bytes(c, n_valid), 256)
+    call = lambda w, out: api.mla_attention_fwd_q4(
+        c, q, lat, q4.codes, q4.scales, q4.slot_frame, n_valid, first, w, out, b.lse,
+        b.workspace[:need], b.dev_status)
+    call(w_uv, b.o)
     torch.cuda.synchronize()
     rollout.check_device_status(b)
-    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert (b.workspace[need:] == 0xFF).all()
+    args = (c, cfg, to_np(plain.cache), plain.slot_frame.cpu().numpy(), to_np(lat), to_np(q),
+            np.zeros(q.shape))
+    out, lse, e_out, e_lse = _reference(*args, to_np(w_uv), first, n_valid)
+    _within(b.o.view(*q.shape[:3], -1), out, e_out, 2.0 ** -8)
+    err = _within(b.lse, lse, e_lse, 0.0)
+    assert np.linalg.norm(err) <= 1e-5 * np.linalg.norm(lse)
+    call(None, b.o_lat)
+    eye = np.broadcast_to(np.eye(d_c), (cfg.n_heads, d_c, d_c))
+    out, lse, e_out, e_lse = _reference(*args, eye, first, n_valid)
+    _within(b.o_lat, out, e_out, 2.0 ** -8)
+    _within(b.lse, lse, e_lse, 0.0)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -20, 300.0, 2.0 ** 100])
+@pytest.mark.parametrize("d_c,d_rope", [(192, 32), (256, 32)])
+def test_queries_of_any_size(d_c, d_rope, size):
+    """bf16's range of queries: rows far outside fp16's, with the score scale to match."""
+    cfg = dataclasses.replace(inputs.with_latent_shape(SMALL, d_c, d_rope), n_heads=2)
+    c, q4, plain = _filled(cfg, api.MLA_PATH_AUTO, 2)
+    first, n_valid = rollout.chunk_schedule(cfg.chunk_frames, cfg.window_frames, 2)
+    lat, (q, w_uv) = _chunk(c, 100), _query(c, 101)
+    q[:, ::3] *= 2.0 ** -6                                  # rows of different sizes
+    q[:, 1::3, :, ::2] *= 2.0 ** -9
+    c.softmax_scale = c.softmax_scale / size
+    big = (q.float() * size).bfloat16()
+    b, plain_b = rollout.ChunkBuffers(c, q4=True), rollout.ChunkBuffers(c, q4=True)
+    api.mla_attention_fwd_q4(c, big, lat, q4.codes, q4.scales, q4.slot_frame, n_valid, first, w_uv,
+                             b.o, b.lse, b.workspace, b.dev_status)
+    c.softmax_scale = cfg.softmax_scale
+    api.mla_attention_fwd_q4(c, q, lat, q4.codes, q4.scales, q4.slot_frame, n_valid, first, w_uv,
+                             plain_b.o, plain_b.lse, plain_b.workspace, plain_b.dev_status)
+    for x, seen in ((b, to_np(big) / size), (plain_b, to_np(q))):     # (a big row is rounded anew)
+        out, lse, e_out, e_lse = _reference(c, cfg, to_np(plain.cache),
+                                            plain.slot_frame.cpu().numpy(), to_np(lat), seen,
+                                            np.zeros(q.shape), to_np(w_uv), first, n_valid)
+        _within(x.o.view(*q.shape[:3], -1), out, e_out, 2.0 ** -8)
+        # (size / size in fp32 leaves 2^-23 of a score)
+        _within(x.lse, lse, e_lse + 2.0 ** -20 * np.abs(lse).max(), 0.0)
 
 
 @pytest.mark.parametrize("chunks", [0, 2, 5])
-@pytest.mark.parametrize("d_c,d_rope", [(192, 32), (128, 64)])
-def test_attention_from_cq_equals_the_call_on_the_rings_values(d_c, d_rope, chunks):
+@pytest.mark.parametrize("d_c,d_rope", [(192, 32), (128, 64), (192, 16)])
+def test_attention_from_cq_matches_the_definition(d_c, d_rope, chunks):
     cfg = inputs.with_latent_shape(SMALL, d_c, d_rope)
     c, q4, plain = _filled(cfg, api.MLA_PATH_AUTO, chunks)
     first, n_valid = rollout.chunk_schedule(cfg.chunk_frames, cfg.window_frames, chunks)
@@ -133,14 +198,61 @@ def test_attention_from_cq_equals_the_call_on_the_rings_values(d_c, d_rope, chun
     c_q = torch.randn((cfg.batch, cfg.n_q, c.d_cq), generator=g, device="cuda").bfloat16()
     w_q = (torch.randn((c.n_heads, cfg.d_latent, c.d_cq), generator=g, device="cuda")
            * c.d_cq ** -0.5).bfloat16()
-    a, b = rollout.ChunkBuffers(c), rollout.ChunkBuffers(c, q4=True)
-    api.mla_attention_fwd_from_cq(c, c_q, w_q, lat, plain.cache, plain.slot_frame, n_valid, first,
-                                  w_uv, a.o, a.lse, a.workspace, a.dev_status)
+    b = rollout.ChunkBuffers(c, q4=True)
     api.mla_attention_fwd_from_cq_q4(c, c_q, w_q, lat, q4.codes, q4.scales, q4.slot_frame, n_valid,
                                      first, w_uv, b.o, b.lse, b.workspace, b.dev_status)
     torch.cuda.synchronize()
     rollout.check_device_status(b)
-    assert torch.equal(a.o, b.o) and torch.equal(a.lse, b.lse)
+    d = oracle.dims_from(cfg)
+    pos = oracle.token_positions(range(first, first + cfg.chunk_frames), d)
+    q = np.einsum("bnk,hdk->bnhd", to_np(c_q), to_np(w_q))
+    size = np.einsum("bnk,hdk->bnhd", np.abs(to_np(c_q)), np.abs(to_np(w_q)))
+    e_q = (c.d_cq + 4) * 2.0 ** -23 * size
+    pair = np.abs(q[..., d_c::2]) + np.abs(q[..., d_c + 1::2])
+    for x in range(cfg.batch):
+        for h in range(cfg.n_heads):
+            q[x, :, h, d_c:] = oracle.rope3d(q[x, :, h, d_c:], pos, d)
+    e_r = e_q[..., d_c::2] + e_q[..., d_c + 1::2] + 2.0 ** -20 * pair
+    e_q[..., d_c:] = np.repeat(e_r, 2, axis=-1)
+    # fp16: 2^-11 of an element, or of a row whose largest is 2^13, half the least step 2^-24
+    e_q += F16 * (np.abs(q) + e_q) + 2.0 ** -38 * np.abs(q).max(-1, keepdims=True)
+    out, lse, e_out, e_lse = _reference(c, cfg, to_np(plain.cache), plain.slot_frame.cpu().numpy(),
+                                        to_np(lat), q, e_q, to_np(w_uv), first, n_valid)
+    _within(b.o.view(*q.shape[:3], -1), out, e_out, 2.0 ** -8)
+    err = _within(b.lse, lse, e_lse, 0.0)
+    assert np.linalg.norm(err) <= 1e-5 * np.linalg.norm(lse)
+
+
+def test_chunk_latents_beyond_fp16():
+    """The chunk's own latents enter the tensor-core attention held at fp16's limits; the ring holds
+    no more than 26880 in any case."""
+    c, q4, _ = _filled(SMALL, api.MLA_PATH_AUTO, 1)
+    lat, (q, w_uv) = _chunk(c, 100), _query(c, 101)
+    outs = []
+    for top in (65504.0, 1e6, 3e38):
+        x = lat.clone()
+        x[0, 7, 5], x[0, 9, 150] = top, -top
+        b = rollout.ChunkBuffers(c, q4=True)
+        api.mla_attention_fwd_q4(c, q * 2.0 ** -12, x, q4.codes, q4.scales, q4.slot_frame, 3, 3, w_uv,
+                                 b.o, b.lse, b.workspace, b.dev_status)
+        outs.append(b.o)
+        assert torch.isfinite(b.o).all()
+    assert torch.equal(outs[1], outs[2])
+
+
+@pytest.mark.parametrize("fuse_uv", [True, False])
+def test_cuda_cores_equal_the_call_on_the_rings_values(fuse_uv):
+    c, q4, plain = _filled(SMALL, api.MLA_PATH_SIMT, 5)
+    first, n_valid = rollout.chunk_schedule(SMALL.chunk_frames, SMALL.window_frames, 5)
+    lat, (q, w_uv) = _chunk(c, 100), _query(c, 101)
+    a, b = rollout.ChunkBuffers(c), rollout.ChunkBuffers(c, q4=True)
+    w = w_uv if fuse_uv else None
+    api.mla_attention_fwd(c, q, lat, plain.cache, plain.slot_frame, n_valid, first, w,
+                          a.o if fuse_uv else a.o_lat, a.lse, a.workspace, a.dev_status)
+    api.mla_attention_fwd_q4(c, q, lat, q4.codes, q4.scales, q4.slot_frame, n_valid, first, w,
+                             b.o if fuse_uv else b.o_lat, b.lse, b.workspace, b.dev_status)
+    assert torch.equal(a.lse, b.lse)
+    assert torch.equal(a.o if fuse_uv else a.o_lat, b.o if fuse_uv else b.o_lat)
 
 
 def test_fp32_ring_on_cuda_cores():
