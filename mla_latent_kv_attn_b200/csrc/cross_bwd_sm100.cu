@@ -167,9 +167,10 @@ template <int D_>
 struct DqShape {
   static constexpr int D = D_;
   static constexpr int kTile = kT * D * 2;
-  static constexpr int kKStages = D == 128 ? 2 : 4;
+  // K_j is held from S(j) to the product with dS(j), almost two steps; V_j for one product
+  static constexpr int kKStages = D == 128 ? 3 : 4;
   static constexpr int kVStages = D == 128 ? 1 : 3;
-  static constexpr int kTiles = 4 + kKStages + kVStages;      // Q and G twice, then the rings
+  static constexpr int kTiles = 3 + kKStages + kVStages;      // Q, G, dQ, then the rings
   static constexpr int kSmem = kTiles * kTile + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -177,14 +178,15 @@ constexpr uint32_t kDqColS = 0, kDqColDP = 128, kDqColAcc = 384;    // dP twice
 
 template <int kKStages, int kVStages>
 struct DqShared {
-  uint64_t qg_full[2], qg_empty[2];       // Q and G of an item (by parity)
+  uint64_t q_full, q_empty;               // the item's Q, read by its last S
+  uint64_t g_full, g_empty;               // the item's G, read by its last dP
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
   uint64_t s_full, s_free;                // S(j) complete; read
   uint64_t dp_full[2], dq_done[2];        // dP(j) complete; the product with dS(j) complete
   uint64_t ds_full;                       // dS(j) in TMEM
   uint64_t acc_free;                      // the item's dQ is in registers
-  uint64_t staged;                        // and in its Q buffer
+  uint64_t staged, stage_free;            // and in shared memory; stored from there
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Sh = DqShape<D>;
   constexpr int kTile = Sh::kTile, kKStages = Sh::kKStages, kVStages = Sh::kVStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t sQ = smem_u32(smem_raw), sG = sQ + 2 * kTile, sK = sG + 2 * kTile;
+  const uint32_t sQ = smem_u32(smem_raw), sG = sQ + kTile, sOut = sG + kTile, sK = sOut + kTile;
   const uint32_t sV = sK + kKStages * kTile;
   auto& sh = *reinterpret_cast<DqShared<kKStages, kVStages>*>(smem_raw + Sh::kTiles * kTile);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -226,9 +228,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
+    mbar_init(smem_u32(&sh.q_full), 1);
+    mbar_init(smem_u32(&sh.q_empty), 1);
+    mbar_init(smem_u32(&sh.g_full), 1);
+    mbar_init(smem_u32(&sh.g_empty), 1);
+    mbar_init(smem_u32(&sh.stage_free), 1);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&sh.qg_full[b]), 1);
-      mbar_init(smem_u32(&sh.qg_empty[b]), 1);
       mbar_init(smem_u32(&sh.dp_full[b]), 1);
       mbar_init(smem_u32(&sh.dq_done[b]), 1);
     }
@@ -269,14 +274,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
         const DqItem w = dq_item(p, it);
         if (w.nt == 0) continue;
-        const int b = n & 1;
-        ok = wait(sh.qg_empty[b], (n >> 1) + 1);
+        ok = wait(sh.q_empty, n + 1);
         if (!ok) break;
-        const uint32_t qb = smem_u32(&sh.qg_full[b]);
-        mbar_arrive_expect_tx(qb, 2 * kTile);
-        load_tile<D>(sQ + b * kTile, &tm_q, qb, w.h, w.q0, w.b);
-        load_tile<D>(sG + b * kTile, &tm_g, qb, w.h, w.q0, w.b);
-        ++n;
+        const uint32_t qb = smem_u32(&sh.q_full), gb = smem_u32(&sh.g_full);
+        mbar_arrive_expect_tx(qb, kTile);
+        load_tile<D>(sQ, &tm_q, qb, w.h, w.q0, w.b);
         for (int j = 0; j < w.nt && ok; ++j, ++t) {
           const int ks = t % kKStages, vs = t % kVStages;
           ok = wait(sh.k_empty[ks], t / kKStages + 1);
@@ -284,12 +286,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t kb = smem_u32(&sh.k_full[ks]);
           mbar_arrive_expect_tx(kb, kTile);
           load_tile<D>(sK + ks * kTile, &tm_k, kb, w.h / p.rep, j * kT, w.b);
+          if (j == 0) {
+            ok = wait(sh.g_empty, n + 1);
+            if (!ok) break;
+            mbar_arrive_expect_tx(gb, kTile);
+            load_tile<D>(sG, &tm_g, gb, w.h, w.q0, w.b);
+          }
           ok = wait(sh.v_empty[vs], t / kVStages + 1);
           if (!ok) break;
           const uint32_t vb = smem_u32(&sh.v_full[vs]);
           mbar_arrive_expect_tx(vb, kTile);
           load_tile<D>(sV + vs * kTile, &tm_v, vb, w.h / p.rep, j * kT, w.b);
         }
+        ++n;
       }
     }
   } else if (warp == kIssuerA) {
@@ -299,13 +308,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
         const DqItem w = dq_item(p, it);
         if (w.nt == 0) continue;
-        ok = wait(sh.qg_full[n & 1], n >> 1);
+        ok = wait(sh.q_full, n);
         for (int j = 0; j < w.nt && ok; ++j, ++t) {
           ok = wait(sh.k_full[t % kKStages], t / kKStages) && (t == 0 || wait(sh.s_free, t - 1));
           if (!ok) break;
           tc_fence_after();
-          mma_tiles<D>(tmem + kDqColS, sQ + (n & 1) * kTile, sK + (t % kKStages) * kTile);
+          mma_tiles<D>(tmem + kDqColS, sQ, sK + (t % kKStages) * kTile);
           mma_commit(smem_u32(&sh.s_full));
+          if (j == w.nt - 1) mma_commit(smem_u32(&sh.q_empty));
         }
         ++n;
       }
@@ -314,24 +324,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t n = 0, t = 0;
       bool ok = true;
-      // dP of tile u (of item n) into buffer u & 1, which the product with dS(u-2) has read
-      const auto issue_dp = [&](uint32_t u) {
+      // dP of tile u into buffer u & 1, which the product with dS(u-2) has read
+      const auto issue_dp = [&](uint32_t u, bool last) {
         if (!wait(sh.v_full[u % kVStages], u / kVStages) ||
             (u >= 2 && !wait(sh.dq_done[u & 1], (u >> 1) - 1)))
           return false;
         tc_fence_after();
-        mma_tiles<D>(tmem + kDqColDP + 128 * (u & 1), sG + (n & 1) * kTile,
-                     sV + (u % kVStages) * kTile);
+        mma_tiles<D>(tmem + kDqColDP + 128 * (u & 1), sG, sV + (u % kVStages) * kTile);
         mma_commit(smem_u32(&sh.v_empty[u % kVStages]));
         mma_commit(smem_u32(&sh.dp_full[u & 1]));
+        if (last) mma_commit(smem_u32(&sh.g_empty));
         return true;
       };
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
         const DqItem w = dq_item(p, it);
         if (w.nt == 0) continue;
-        ok = wait(sh.qg_full[n & 1], n >> 1) && issue_dp(t);
+        ok = wait(sh.g_full, n) && issue_dp(t, w.nt == 1);
         for (int j = 0; j < w.nt && ok; ++j, ++t) {
-          if (j + 1 < w.nt) ok = issue_dp(t + 1);
+          if (j + 1 < w.nt) ok = issue_dp(t + 1, j + 2 == w.nt);
           ok = ok && wait(sh.ds_full, t) && (j > 0 || n == 0 || wait(sh.acc_free, n - 1));
           if (!ok) break;
           tc_fence_after();
@@ -353,10 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait(sh.staged, n);
         if (!ok) break;
         for (int k = 0; k < D / 64; ++k)           // (rows past n_q are not written)
-          tma_store_4d(&tm_dq, sQ + (n & 1) * kTile + k * kT * 128, 64 * k, w.h, w.q0, w.b);
+          tma_store_4d(&tm_dq, sOut + k * kT * 128, 64 * k, w.h, w.q0, w.b);
         bulk_commit_group();
         bulk_wait_group_read<0>();
-        mbar_arrive(smem_u32(&sh.qg_empty[n & 1]));
+        mbar_arrive(smem_u32(&sh.stage_free));
         ++n;
       }
       bulk_wait_group_all();
@@ -432,10 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(smem_u32(&sh.ds_full));
       }
       if (!ok) break;
-      ok = wait_all(sh.dq_done[(t - 1) & 1], (t - 1) >> 1);
+      ok = wait_all(sh.dq_done[(t - 1) & 1], (t - 1) >> 1) &&
+           (n == 0 || wait_all(sh.stage_free, n - 1));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t stage = sQ + (n & 1) * kTile;
 #pragma unroll 1
       for (int c = 0; c < D / 2; c += 32) {
         uint32_t r[32];
@@ -447,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             v[e] = pack_bf16x2(__uint_as_float(r[8 * k + 2 * e]), __uint_as_float(r[8 * k + 2 * e + 1]));
-          store_shared16(swizzled_piece(stage + (col / 64) * kT * 128, row, (col % 64) / 8 + k), v);
+          store_shared16(swizzled_piece(sOut + (col / 64) * kT * 128, row, (col % 64) / 8 + k), v);
         }
       }
       tc_fence_before();
@@ -491,12 +501,14 @@ struct DkvShared {
   int abort_flag;
 };
 
-// A block per split, state tile, key head and sample.  Roles (352 threads): warps 0-7 softmax, 8 TMA
-// producer, 9 issuer of S^T and dV, 10 issuer of dP^T and dK.  S^T(i+1) may run once dV(i) has read
-// P^T(i), which the softmax writes before it turns to dS: while dS(i) is being computed the tensor
-// cores have dV(i) and S^T(i+1), and while P(i+1) is, dK(i) and dP^T(i+1).
+// A block per split, state tile, key head and sample.  Roles (320 threads): warps 0-7 softmax, 8 TMA
+// producer, 9 issuer.  S^T(i+1) may run once dV(i) has read P^T(i), which the softmax writes before
+// it turns to dS: while dS(i) is being computed the tensor cores have dV(i) and S^T(i+1), and while
+// P(i+1) is, dK(i) and dP^T(i+1).  The step is bound by the chain P, dV, S^T, so one thread issues
+// in that order (two threads, one per pair, interleaved dK with S^T: 3600 cycles a step against
+// 2048 of products).
 // Rows of masked states hold whatever their scores gave; they reach no other row and are not used.
-constexpr int kThreadsKV = 352;
+constexpr int kThreadsKV = 320;
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsKV, 1)
@@ -525,7 +537,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
       mbar_init(smem_u32(&sh.q_full[s]), 1);
       mbar_init(smem_u32(&sh.q_empty[s]), 1);
       mbar_init(smem_u32(&sh.g_full[s]), 1);
-      mbar_init(smem_u32(&sh.g_empty[s]), 2);      // dP^T and dV
+      mbar_init(smem_u32(&sh.g_empty[s]), 1);
     }
     mbar_init(smem_u32(&sh.s_full), 1);
     mbar_init(smem_u32(&sh.dp_full), 1);
@@ -591,38 +603,39 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
   } else if (warp == kIssuerA) {
     if (lane == 0) {
       bool ok = wait(sh.k_full, 0);
-      for (int i = 0; i < n && ok; ++i) {
+      const auto issue_s = [&](int i) {
         const int s = i % kStages;
-        ok = wait(sh.q_full[s], i / kStages) && (i == 0 || wait(sh.dv_done, i - 1));
-        if (!ok) break;
+        if (!wait(sh.q_full[s], i / kStages)) return false;
         tc_fence_after();
         mma_tiles<D>(tmem + kColS, sK, sQ + s * kTile);
         mma_commit(smem_u32(&sh.s_full));
-        ok = wait(sh.g_full[s], i / kStages) && wait(sh.p_full, i);
+        return true;
+      };
+      const auto issue_dp = [&](int i) {
+        const int s = i % kStages;
+        if (!wait(sh.g_full[s], i / kStages)) return false;
+        tc_fence_after();
+        mma_tiles<D>(tmem + kColDP, sV, sG + s * kTile);
+        mma_commit(smem_u32(&sh.dp_full));
+        return true;
+      };
+      ok = ok && issue_s(0) && wait(sh.v_full, 0) && issue_dp(0);
+      for (int i = 0; i < n && ok; ++i) {
+        const int s = i % kStages;
+        ok = wait(sh.p_full, i);
         if (!ok) break;
         tc_fence_after();
         mma_pairs_by_tile<D>(tmem + kColDV, tmem + kColS, sG + s * kTile, i > 0);
         mma_commit(smem_u32(&sh.g_empty[s]));
         mma_commit(smem_u32(&sh.dv_done));
-      }
-    }
-  } else if (warp == kIssuerB) {
-    if (lane == 0) {
-      bool ok = wait(sh.v_full, 0);
-      for (int i = 0; i < n && ok; ++i) {
-        const int s = i % kStages;
-        ok = wait(sh.g_full[s], i / kStages) && (i == 0 || wait(sh.dk_done, i - 1));
-        if (!ok) break;
-        tc_fence_after();
-        mma_tiles<D>(tmem + kColDP, sV, sG + s * kTile);
-        mma_commit(smem_u32(&sh.g_empty[s]));
-        mma_commit(smem_u32(&sh.dp_full));
-        ok = wait(sh.ds_full, i);
+        ok = i + 1 == n || (wait(sh.dv_done, i) && issue_s(i + 1));
+        ok = ok && wait(sh.ds_full, i);
         if (!ok) break;
         tc_fence_after();
         mma_pairs_by_tile<D>(tmem + kColDK, tmem + kColDP, sQ + s * kTile, i > 0);
         mma_commit(smem_u32(&sh.q_empty[s]));
         mma_commit(smem_u32(&sh.dk_done));
+        ok = i + 1 == n || (wait(sh.dk_done, i) && issue_dp(i + 1));
       }
     }
   } else {
