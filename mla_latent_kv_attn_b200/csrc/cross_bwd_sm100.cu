@@ -381,8 +381,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint32_t n = 0, t = 0;
     bool ok = true;
+    // item and row statistics are read an item ahead
+    const auto stat_at = [&](const DqItem& w) {
+      return (static_cast<int64_t>(w.b) * p.H + w.h) * p.n_pad + w.q0 + row;
+    };
+    DqItem next = dq_item(p, blockIdx.x);
+    float next_l = p.lse2[stat_at(next)], next_d = p.delta[stat_at(next)];
     for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-      const DqItem w = dq_item(p, it);
+      const DqItem w = next;
+      const float nl = -next_l, row_delta = next_d;
+      if (it + gridDim.x < p.items) {
+        next = dq_item(p, it + gridDim.x);
+        next_l = p.lse2[stat_at(next)];
+        next_d = p.delta[stat_at(next)];
+      }
       if (w.nt == 0) {
         const int i = w.q0 + row;
         if (i < p.n_q) {
@@ -392,10 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      const int64_t sr = (static_cast<int64_t>(w.b) * p.H + w.h) * p.n_pad + w.q0 + row;
-      const float nl = -p.lse2[sr];
       // a single state's softmax is constant: its dS is zero
-      const float sc = w.len == 1 ? 0.f : p.scale, nd = -p.delta[sr] * sc;
+      const float sc = w.len == 1 ? 0.f : p.scale, nd = -row_delta * sc;
       const uint64_t nl2 = f2_pack(nl, nl), sc2 = f2_pack(sc, sc), nd2 = f2_pack(nd, nd);
       for (int j = 0; j < w.nt; ++j, ++t) {
         ok = wait_all(sh.s_full, t);
