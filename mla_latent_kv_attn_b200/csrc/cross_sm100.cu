@@ -99,7 +99,10 @@ struct Item {
   int b, h, q0, len, nt;
 };
 
+// Item `it` (the last one when there is none).  Every role decodes an item ahead of its work: the
+// length comes from global memory, some 700 cycles away.
 __device__ __forceinline__ Item item_of(const CrossFwdParams& p, int it) {
+  it = min(it, p.items - 1);
   Item w;
   w.q0 = (it % p.pairs) * 2 * kBM;
   const int bh = it / p.pairs;
@@ -215,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto wait = [&](uint64_t& bar, uint32_t phase) {
     return mbar_wait_or_abort(smem_u32(&bar), phase & 1, abort_flag, p.dev_status);
   };
+  Item next = item_of(p, blockIdx.x);
 
   if (warp == kProducerWarp) {
     if (lane == 0) {
@@ -224,7 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n_item[2] = {0, 0}, u = 0;          // items of the streams, uses of the ring
       bool ok = true;
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-        const Item w = item_of(p, it);
+        const Item w = next;
+        next = item_of(p, it + gridDim.x);
         if (w.nt == 0) continue;
         for (int i = 0; i < 2 && ok; ++i) {
           if (w.q0 + i * kBM >= p.n_q) break;
@@ -256,7 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n_item[2] = {0, 0};
       bool ok = true;
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-        const Item w = item_of(p, it);
+        const Item w = next;
+        next = item_of(p, it + gridDim.x);
         if (w.nt == 0) continue;
         for (int i = 0; i < 2; ++i) {
           if (w.q0 + i * kBM >= p.n_q) break;
@@ -297,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(smem_u32(&s_full[i]));
       };
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-        const Item w = item_of(p, it);
+        const Item w = next;
+        next = item_of(p, it + gridDim.x);
         if (w.nt == 0) continue;
         if (w.q0 + i * kBM >= p.n_q) {     // no rows for this stream: release what it would read
           for (int j = 0; j < 2 * w.nt && ok; ++j, ++u0) {
@@ -368,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t t = 0, u0 = 0, n_item = 0;
     bool ok = true;
     for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-      const Item w = item_of(p, it);
+      const Item w = next;
+      next = item_of(p, it + gridDim.x);
       if (w.nt == 0) {
         const int n = w.q0 + i * kBM + row;
         if (n < p.n_q) {
