@@ -57,7 +57,7 @@ struct FwdShape {
   static constexpr int kSmem = (4 + kStages) * kTile + 3072;      // tiles, then FwdShared
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // Pairs (out of every 8) whose exponentials take the FMA-pipe polynomial instead of the SFU.
-  static constexpr int kPolyPairs = 2;
+  static constexpr int kPolyPairs = 0;
   static constexpr bool kAliasP = D == 128;               // P in the columns of its S buffer
   static constexpr uint32_t s_col(int i) { return 128u * i; }
   // 32 columns of P for half `ch` of the states
@@ -113,13 +113,16 @@ __device__ __forceinline__ Item item_of(const CrossFwdParams& p, int it) {
   return w;
 }
 
-// The largest of 32 scores; those from `valid` on become -infinity.
-__device__ __forceinline__ float masked_max(uint32_t (&s)[32], int valid) {
+// Scores from column `valid` on become -infinity.
+__device__ __forceinline__ void mask_scores(uint32_t (&s)[32], int valid) {
   if (valid < 32) {
 #pragma unroll
     for (int c = 0; c < 32; ++c)
       if (c >= valid) s[c] = 0xff800000u;
   }
+}
+
+__device__ __forceinline__ float max_score(const uint32_t (&s)[32]) {
   float m4[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -132,14 +135,16 @@ __device__ __forceinline__ float masked_max(uint32_t (&s)[32], int valid) {
   return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
 }
 
-// p = 2^(s scale - m) of kN consecutive scores of a row, packed to bf16 pairs; returns their sum.
-template <int kN, int kPolyPairs>
-__device__ __forceinline__ float exp_pairs(const uint32_t* s, float scale_log2, float m,
-                                           uint32_t* w) {
+// p = 2^(s scale - m) of 32 consecutive scores of a row, packed to bf16 pairs; returns their sum.
+// (A masked score gives 0, or 2^-125 where the polynomial holds its argument: nothing beside the
+// row's largest, 1 or more, and its value row is zero.)
+template <int kPolyPairs>
+__device__ __forceinline__ float exp_pairs(const uint32_t (&s)[32], float scale_log2, float m,
+                                           uint32_t (&w)[16]) {
   const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-m, -m);
-  uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+  uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
-  for (int i = 0; i < kN / 2; ++i) {
+  for (int i = 0; i < 16; ++i) {
     float x0, x1, p0, p1;
     f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, nm2),
               x0, x1);
@@ -149,11 +154,11 @@ __device__ __forceinline__ float exp_pairs(const uint32_t* s, float scale_log2, 
       p0 = fast_exp2(x0);
       p1 = fast_exp2(x1);
     }
-    sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(p0, p1));
+    sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
     w[i] = pack_bf16x2(p0, p1);
   }
   float l0, l1;
-  f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), l0, l1);
+  f2_unpack(f2_add(sum2[0], sum2[1]), l0, l1);
   return l0 + l1;
 }
 
@@ -401,9 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mx = -INFINITY;
         if (ok) {
           tmem_ld32_wait(ts + 32, s);
-          mx = masked_max(s, valid - 32);
+          mask_scores(s, valid - 32);
+          mx = max_score(s);
           tmem_ld32_wait(ts, s);
-          mx = fmaxf(mx, masked_max(s, valid)) * p.scale_log2;
+          mask_scores(s, valid);
+          mx = fmaxf(mx, max_score(s)) * p.scale_log2;
         }
         // The other half's maximum.  Every thread of the stream passes this barrier in every tile,
         // and all of them leave here if a wait of one ran out.
@@ -438,8 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(to + c, r);
           }
         }
-        const bool ragged = w.len - j * kBN < kBN;
-        if (ragged && w.len < p.n_kv) {
+        if (w.len - j * kBN < kBN && w.len < p.n_kv) {
           // the value rows of this half's masked states (both streams write the same zeros)
           const uint32_t uv = u0 + 2 * j + 1;
           if (ok) ok = wait_all(kv_full[uv % kStages], uv / kStages);
@@ -448,17 +454,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
         }
         uint32_t pw[16];
-        l += ragged ? exp_pairs<32, 0>(s, p.scale_log2, m, pw)
-                    : exp_pairs<32, Sh::kPolyPairs>(s, p.scale_log2, m, pw);
+        l += exp_pairs<Sh::kPolyPairs>(s, p.scale_log2, m, pw);
         tmem_ld32_wait(ts + 32, s);
         if constexpr (!Sh::kAliasP) {
           tc_fence_before();
           mbar_arrive(smem_u32(&s_free[i]));
         }
         tmem_st16(tp, pw);
-        if (ragged) masked_max(s, valid - 32);
-        l += ragged ? exp_pairs<32, 0>(s, p.scale_log2, m, pw)
-                    : exp_pairs<32, Sh::kPolyPairs>(s, p.scale_log2, m, pw);
+        mask_scores(s, valid - 32);
+        l += exp_pairs<Sh::kPolyPairs>(s, p.scale_log2, m, pw);
         tmem_st16(tp + 16, pw);
         tmem_wait_st();
         tc_fence_before();
