@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (w.len - j * kT < kT && w.len < p.n_kv) {
           // the product reads the keys of masked states: this half's rows become zeros
-          zero_rows<D / 64>(sK + (t % kKStages) * kTile, 64 * ch + max(valid, 0), 64 * ch + 64,
+          zero_rows<D / 64, kT>(sK + (t % kKStages) * kTile, 64 * ch + max(valid, 0), 64 * ch + 64,
                             threadIdx.x % 128, 128);
           fence_proxy_async_smem();
         }

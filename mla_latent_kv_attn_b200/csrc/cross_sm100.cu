@@ -5,25 +5,21 @@
 // streams of 128 rows that share every key and value tile: while one stream's softmax runs on the
 // CUDA cores, the other's products run on the tensor cores.  (With 128 rows per item the keys and
 // values would cross L2 -> SM twice as often, 114 MB in the call of 4680 queries, 12 heads and 512
-// states, whose products take 9 us.)  Roles (640 threads):
-//   warps 0-15    softmax; stream = warp / 8, and within a stream two warps share 32 TMEM lanes
-//                 (query rows), each with half of a tile's states.  Online softmax in the log2
-//                 domain, the halves' maxima exchanged through shared memory, O rescaled only when
-//                 a row's maximum grows by more than 2^8; P rounded to bf16 (the tensor cores'
-//                 operand type; the row sum l is taken from the unrounded values in fp32); O / l
-//                 into shared memory, lse
-//   warp 16       TMA producer: the item's two Q tiles (into the buffer that the item before last
-//                 left), then K_0, V_0, K_1, V_1, ... (128 states each) through a ring of stages
-//   warps 17, 18  MMA issuer of stream 0, 1: S = Q K_j^T (both in shared memory) and
+// states, whose products take 9 us.)  Roles (384 threads):
+//   warps 0-3, 4-7  softmax of stream 0, 1, one TMEM lane (query row) per thread: online softmax in
+//                 the log2 domain, O rescaled only when a row's maximum grows by more than 2^8; P
+//                 rounded to bf16 (the tensor cores' operand type; the row sum l is taken from the
+//                 unrounded values in fp32); O / l into shared memory, lse
+//   warp 8        TMA producer: the item's two Q tiles (into the buffer that the item before last
+//                 left), then K_0, V_0, K_1, V_1, ... (80 states each) through a ring of stages
+//   warps 9, 10   MMA issuer of stream 0, 1: S = Q K_j^T (both in shared memory) and
 //                 O += P_j V_j (P in TMEM, V read MN-major)
-//   warp 19       TMA stores of O from the item's Q buffer.  (Stored by the softmax threads, 16
+//   warp 11       TMA stores of O from the item's Q buffer.  (Stored by the softmax threads, 16
 //                 bytes of 32 rows at a time, O took 9000 cycles an item.)
-// TMEM, 512 columns: two S buffers, two O accumulators and, for d 64, two P buffers; QK(j+1) then
-// runs under the softmax of j.  For d 128 nothing is left for P and it takes the place of S: each
-// half of the states' 64 columns become 32 columns of bf16 pairs (written by the threads that read
-// them), and QK(j+1) waits for PV(j).  A thread holds 32 scores at a time and reads S up to twice: with 64
-// in registers (96 a thread) the spills went past the little L1 that the tiles leave, and a tile's
-// softmax took 4000 cycles.
+// A tile has 80 states: S (80 columns) and P (40) of a stream then fit beside an O of 128, all of TMEM
+// with two streams, and QK(j+1) runs under the softmax of j.  With 128 states P has to take the place
+// of S, and a step is the chain QK, softmax, PV: 4900 cycles a pair of tiles of 128, against 2048 of
+// products.
 // An item's first QK of stream 1 waits for that of stream 0: streams in step would load the tensor
 // and the CUDA cores in turn (6000 cycles a pair of tiles, against 2048 of products and 4500 as it is).
 // States past a sample's length are masked: their scores become -infinity by selection, and their
@@ -37,12 +33,13 @@ namespace {
 using namespace sm100;
 
 constexpr int kBM = kCrossTile;      // query rows of a stream
-constexpr int kBN = kCrossTile;      // states of a tile
-constexpr int kStreamThreads = 256;
-constexpr int kProducerWarp = 16;
-constexpr int kIssuerWarp = 17;      // and 18; warp 17 also allocates TMEM
-constexpr int kStoreWarp = 19;
-constexpr int kThreads = 640;
+constexpr int kBN = 80;              // states of a tile
+constexpr int kHalf = kBN / 2;
+constexpr int kStreamThreads = 128;
+constexpr int kProducerWarp = 8;
+constexpr int kIssuerWarp = 9;       // and 10; warp 9 also allocates TMEM
+constexpr int kStoreWarp = 11;
+constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -52,20 +49,18 @@ struct FwdShape {
   static_assert(D == 64 || D == 128, "head width");
   static constexpr int kBlocks = D / 64;                  // 64-column blocks, 128B swizzle
   static constexpr int kBlk = kBM * 128;                  // 16 KB
-  static constexpr int kTile = kBlocks * kBlk;
-  static constexpr int kStages = D == 128 ? 3 : 8;
-  static constexpr int kSmem = (4 + kStages) * kTile + 3072;      // tiles, then FwdShared
+  static constexpr int kTile = kBlocks * kBlk;            // Q, O
+  static constexpr int kKvBlk = kBN * 128;                // 10 KB
+  static constexpr int kKvTile = kBlocks * kKvBlk;
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kTileBytes = 4 * kTile + kStages * kKvTile;
+  static constexpr int kSmem = kTileBytes + 1024;         // tiles, then FwdShared
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  // Pairs (out of every 8) whose exponentials take the FMA-pipe polynomial instead of the SFU.
-  static constexpr int kPolyPairs = 0;
-  static constexpr bool kAliasP = D == 128;               // P in the columns of its S buffer
-  static constexpr uint32_t s_col(int i) { return 128u * i; }
-  // 32 columns of P for half `ch` of the states
-  static constexpr uint32_t p_col(int i, int ch) {
-    return kAliasP ? s_col(i) + 64u * ch : 256u + 64u * i + 32u * ch;
-  }
-  static constexpr uint32_t o_col(int i) { return kAliasP ? 256u + 128u * i : 384u + 64u * i; }
 };
+// TMEM columns of stream i
+__host__ __device__ constexpr uint32_t s_col(int i) { return 128u * i; }
+__host__ __device__ constexpr uint32_t p_col(int i) { return 128u * i + kBN; }
+__host__ __device__ constexpr uint32_t o_col(int i) { return 256u + 128u * i; }
 
 struct CrossFwdParams {
   int n_q, H, rep, n_kv, pairs;      // pairs: items per (sample, head)
@@ -83,17 +78,16 @@ struct FwdShared {
   uint64_t q_full[2][2], q_empty[2][2];     // [stream][buffer]
   uint64_t kv_full[kStages], kv_empty[kStages];
   uint64_t s_full[2];        // S(j) complete
-  uint64_t s_free[2];        // S(j) has been read (when P has its own columns)
-  uint64_t p_full[2][2];     // states 0-63, 64-127 of P(j) are in TMEM
+  uint64_t s_free[2];        // S(j) has been read
+  uint64_t p_full[2][2];     // each half of the states of P(j) is in TMEM
   uint64_t pv_done[2];       // PV(j) complete
   uint64_t o_free[2];        // the item's O is in registers
   uint64_t o_staged[2];      // and in the item's Q buffer
   uint64_t first_qk[2];      // stream 0's first S of an item (by parity)
-  float part[2][2][kBM];     // [stream][half]: row maxima, row sums
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(FwdShared<8>) <= 3072, "shared memory");
+static_assert(sizeof(FwdShared<8>) <= 1024, "shared memory");
 
 struct Item {
   int b, h, q0, len, nt;
@@ -113,52 +107,41 @@ __device__ __forceinline__ Item item_of(const CrossFwdParams& p, int it) {
   return w;
 }
 
-// Scores from column `valid` on become -infinity.
-__device__ __forceinline__ void mask_scores(uint32_t (&s)[32], int valid) {
-  if (valid < 32) {
+// The largest of a row's scores; those from `valid` on become -infinity.
+__device__ __forceinline__ float masked_max(uint32_t (&s)[kBN], int valid) {
+  if (valid < kBN) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
+    for (int c = 0; c < kBN; ++c)
       if (c >= valid) s[c] = 0xff800000u;
   }
-}
-
-__device__ __forceinline__ float max_score(const uint32_t (&s)[32]) {
-  float m4[4];
+  float m8[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float a = fmax3(__uint_as_float(s[k]), __uint_as_float(s[k + 4]), __uint_as_float(s[k + 8]));
+  for (int k = 0; k < 8; ++k) {
+    float a = __uint_as_float(s[k]);
 #pragma unroll
-    for (int c = 12; c < 28; c += 8)
-      a = fmax3(a, __uint_as_float(s[c + k]), __uint_as_float(s[c + 4 + k]));
-    m4[k] = fmaxf(a, __uint_as_float(s[28 + k]));
+    for (int c = 8; c + 8 < kBN; c += 16)
+      a = fmax3(a, __uint_as_float(s[c + k]), __uint_as_float(s[c + 8 + k]));
+    m8[k] = kBN / 8 % 2 ? a : fmaxf(a, __uint_as_float(s[kBN - 8 + k]));
   }
-  return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+  return fmaxf(fmax3(fmax3(m8[0], m8[1], m8[2]), m8[3], m8[4]), fmax3(m8[5], m8[6], m8[7]));
 }
 
-// p = 2^(s scale - m) of 32 consecutive scores of a row, packed to bf16 pairs; returns their sum.
-// (A masked score gives 0, or 2^-125 where the polynomial holds its argument: nothing beside the
-// row's largest, 1 or more, and its value row is zero.)
-template <int kPolyPairs>
-__device__ __forceinline__ float exp_pairs(const uint32_t (&s)[32], float scale_log2, float m,
-                                           uint32_t (&w)[16]) {
+// p = 2^(s scale - m) of half of a row's scores, packed to bf16 pairs; returns their sum.
+__device__ __forceinline__ float exp_pairs(const uint32_t* s, float scale_log2, float m,
+                                           uint32_t (&w)[kHalf / 2]) {
   const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-m, -m);
-  uint64_t sum2[2] = {0ull, 0ull};
+  uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float x0, x1, p0, p1;
+  for (int i = 0; i < kHalf / 2; ++i) {
+    float x0, x1;
     f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, nm2),
               x0, x1);
-    if ((i & 7) < kPolyPairs) {
-      exp2_poly_pair(x0, x1, p0, p1);
-    } else {
-      p0 = fast_exp2(x0);
-      p1 = fast_exp2(x1);
-    }
-    sum2[i & 1] = f2_add(sum2[i & 1], f2_pack(p0, p1));
+    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+    sum2[i & 3] = f2_add(sum2[i & 3], f2_pack(p0, p1));
     w[i] = pack_bf16x2(p0, p1);
   }
   float l0, l1;
-  f2_unpack(f2_add(sum2[0], sum2[1]), l0, l1);
+  f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), l0, l1);
   return l0 + l1;
 }
 
@@ -170,10 +153,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tm_o, CrossFwdParams p) {
   using Sh = FwdShape<D>;
   constexpr int kStages = Sh::kStages, kTile = Sh::kTile, kBlk = Sh::kBlk;
+  constexpr int kKvTile = Sh::kKvTile, kKvBlk = Sh::kKvBlk;
   // (the declared alignment is the swizzle's; there is no shared memory beside this)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sQ = smem_u32(smem_raw), sKV = sQ + 4 * kTile;  // Q buffer b of stream i: 2 i + b
-  FwdShared<kStages>& sh = *reinterpret_cast<FwdShared<kStages>*>(smem_raw + (4 + kStages) * kTile);
+  FwdShared<kStages>& sh = *reinterpret_cast<FwdShared<kStages>*>(smem_raw + Sh::kTileBytes);
   auto& q_full = sh.q_full;
   auto& q_empty = sh.q_empty;
   auto& kv_full = sh.kv_full;
@@ -194,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int b = 0; b < 2; ++b) {
         mbar_init(smem_u32(&q_full[i][b]), 1);
         mbar_init(smem_u32(&q_empty[i][b]), 1);
-        mbar_init(smem_u32(&p_full[i][b]), kBM);
+        mbar_init(smem_u32(&p_full[i][b]), kStreamThreads);
       }
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&s_free[i]), kStreamThreads);
@@ -253,9 +237,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(kv_empty[s], u / kStages + 1);
           if (!ok) break;
           const uint32_t fb = smem_u32(&kv_full[s]);
-          mbar_arrive_expect_tx(fb, kTile);
+          mbar_arrive_expect_tx(fb, kKvTile);
           for (int k = 0; k < Sh::kBlocks; ++k)
-            tma_load_4d(sKV + s * kTile + k * kBlk, j & 1 ? &tm_v : &tm_k, fb, 64 * k, w.h / p.rep,
+            tma_load_4d(sKV + s * kKvTile + k * kKvBlk, j & 1 ? &tm_v : &tm_k, fb, 64 * k, w.h / p.rep,
                         (j >> 1) * kBN, w.b);
         }
       }
@@ -291,19 +275,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc_pv = idesc_bf16_f32(kBM, D, 0, 1);
       const uint64_t qd0 = smem_desc(sQ + 2 * i * kTile, 16, 1024, kSwizzle128B);
       const uint64_t kd0 = smem_desc(sKV, 16, 1024, kSwizzle128B);
-      const uint64_t vd0 = smem_desc(sKV, kBlk, 1024, kSwizzle128B);
-      const uint32_t ts = tmem + Sh::s_col(i), to = tmem + Sh::o_col(i);
+      const uint64_t vd0 = smem_desc(sKV, kKvBlk, 1024, kSwizzle128B);
+      const uint32_t ts = tmem + s_col(i), tp = tmem + p_col(i), to = tmem + o_col(i);
       uint32_t n_item = 0, t = 0, u0 = 0;   // items and tiles of this stream, uses of the ring
       uint32_t n_both = 0;                  // items in which both streams have rows
       bool ok = true;
       const auto issue_qk = [&](uint32_t u) {
         const uint64_t qd = qd0 + ((n_item & 1) * kTile >> 4);
-        const uint64_t kd = kd0 + ((u % kStages) * kTile >> 4);
+        const uint64_t kd = kd0 + ((u % kStages) * kKvTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * kBlk >> 4) + 2 * (kk & 3);
-          mma_ss(ts, qd + off, kd + off, idesc_qk, kk ? 1u : 0u);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(ts, qd + (((kk >> 2) * kBlk >> 4) + 2 * (kk & 3)),
+                 kd + (((kk >> 2) * kKvBlk >> 4) + 2 * (kk & 3)), idesc_qk, kk ? 1u : 0u);
         mma_commit(smem_u32(&kv_empty[u % kStages]));
         mma_commit(smem_u32(&s_full[i]));
       };
@@ -325,17 +308,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i == 1) ok = ok && wait(first_qk[n_both & 1], n_both >> 1);
         for (int j = 0; j < w.nt && ok; ++j) {
           const uint32_t uk = u0 + 2 * j, uv = uk + 1;
-          if (Sh::kAliasP || j == 0) {
-            // the S buffer: PV of the last tile has read P out of it, or (P in its own columns)
-            // the softmax has read that tile's S
-            ok = wait(kv_full[uk % kStages], uk / kStages) &&
-                 (t == 0 || wait(Sh::kAliasP ? pv_done[i] : s_free[i], t - 1));
+          if (j == 0) {
+            ok = wait(kv_full[uk % kStages], uk / kStages) && (t == 0 || wait(s_free[i], t - 1));
             if (!ok) break;
             tc_fence_after();
             issue_qk(uk);
-            if (i == 0 && j == 0 && both) mma_commit(smem_u32(&first_qk[n_both & 1]));
+            if (i == 0 && both) mma_commit(smem_u32(&first_qk[n_both & 1]));
           }
-          if (!Sh::kAliasP && j + 1 < w.nt) {
+          if (j + 1 < w.nt) {
             const uint32_t un = uk + 2;
             ok = wait(kv_full[un % kStages], un / kStages) && wait(s_free[i], t);
             if (!ok) break;
@@ -344,16 +324,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ok = wait(kv_full[uv % kStages], uv / kStages) &&
                (j > 0 || n_item == 0 || wait(o_free[i], n_item - 1));
-          const uint64_t vd = vd0 + ((uv % kStages) * kTile >> 4);
+          const uint64_t vd = vd0 + ((uv % kStages) * kKvTile >> 4);
           for (int half = 0; half < 2 && ok; ++half) {
             ok = wait(p_full[i][half], t);
             if (!ok) break;
             tc_fence_after();
+            // (the states of a k-step that spans the halves come with the second)
 #pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
-              const int kk = 4 * half + k4;
-              mma_ts(to, tmem + Sh::p_col(i, half) + 8 * k4, vd + 128 * kk, idesc_pv, (j | kk) != 0 ? 1u : 0u);
-            }
+            for (int kk = 0; kk < kBN / 16; ++kk)
+              if ((16 * kk + 15 >= kHalf) == (half == 1))
+                mma_ts(to, tp + 8 * kk, vd + 128 * kk, idesc_pv, (j | kk) != 0 ? 1u : 0u);
           }
           if (!ok) break;
           mma_commit(smem_u32(&kv_empty[uv % kStages]));
@@ -367,13 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ softmax
-    const int i = warp / 8, ch = (warp / 4) & 1;         // stream, half of the states
+    const int i = warp / 4;                              // stream
     const int row = (warp % 4) * 32 + lane;              // TMEM lane
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-    const uint32_t ts = tl + Sh::s_col(i) + 64 * ch, tp = tl + Sh::p_col(i, ch);
-    const uint32_t to = tl + Sh::o_col(i) + D / 2 * ch;
-    float* mine = &sh.part[i][ch][row];
-    const float* other = &sh.part[i][ch ^ 1][row];
+    const uint32_t ts = tl + s_col(i), tp = tl + p_col(i), to = tl + o_col(i);
     const auto wait_all = [&](uint64_t& bar, uint32_t phase) {
       return __all_sync(0xffffffffu, wait(bar, phase)) != 0;
     };
@@ -386,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = w.q0 + i * kBM + row;
         if (n < p.n_q) {
           uint4* o4 = reinterpret_cast<uint4*>(
-              p.out + ((static_cast<int64_t>(w.b) * p.n_q + n) * p.H + w.h) * D + D / 2 * ch);
-          for (int c = 0; c < D / 16; ++c) o4[c] = make_uint4(0u, 0u, 0u, 0u);
-          if (p.lse != nullptr && ch == 0)
+              p.out + ((static_cast<int64_t>(w.b) * p.n_q + n) * p.H + w.h) * D);
+          for (int c = 0; c < D / 8; ++c) o4[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (p.lse != nullptr)
             p.lse[(static_cast<int64_t>(w.b) * p.H + w.h) * p.n_q + n] = -INFINITY;
         }
         continue;
@@ -400,25 +377,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = 0.f, l = 0.f;
       for (int j = 0; j < w.nt; ++j, ++t) {
         ok = wait_all(s_full[i], t);
-        tc_fence_after();
-        const int valid = w.len - j * kBN - 64 * ch;     // of this thread's 64 states
-        uint32_t s[32];
-        float mx = -INFINITY;
-        if (ok) {
-          tmem_ld32_wait(ts + 32, s);
-          mask_scores(s, valid - 32);
-          mx = max_score(s);
-          tmem_ld32_wait(ts, s);
-          mask_scores(s, valid);
-          mx = fmaxf(mx, max_score(s)) * p.scale_log2;
-        }
-        // The other half's maximum.  Every thread of the stream passes this barrier in every tile,
-        // and all of them leave here if a wait of one ran out.
-        *mine = mx;
-        tc_fence_before();
-        ok = !named_bar_or(1 + i, kStreamThreads, !ok);
         if (!ok) break;
-        mx = fmaxf(mx, *other);
+        tc_fence_after();
+        const int valid = w.len - j * kBN;
+        uint32_t s[kBN];
+        tmem_ld80_wait(ts, s);
+        tc_fence_before();
+        mbar_arrive(smem_u32(&s_free[i]));
+        const float mx = masked_max(s, valid) * p.scale_log2;
         float alpha = 1.f;
         bool rescale = false;
         if (j == 0) {
@@ -430,14 +396,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = m_new;
           rescale = true;
         }
-        // O and P's buffer are free once PV(j-1) is complete; with P in S's columns QK(j) waited
-        if (!Sh::kAliasP && t > 0) {
-          if (ok) ok = wait_all(pv_done[i], t - 1);
+        uint32_t pw[kHalf / 2];
+        l += exp_pairs(s, p.scale_log2, m, pw);
+        // O and P's buffer are free once PV(j-1) is complete
+        if (t > 0) {
+          ok = wait_all(pv_done[i], t - 1);
+          if (!ok) break;
           tc_fence_after();
         }
         if (rescale) {
 #pragma unroll 1
-          for (int c = 0; c < D / 2; c += 16) {
+          for (int c = 0; c < D; c += 16) {
             uint32_t r[16];
             tmem_ld16_wait(to + c, r);
 #pragma unroll
@@ -445,49 +414,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(to + c, r);
           }
         }
-        if (w.len - j * kBN < kBN && w.len < p.n_kv) {
-          // the value rows of this half's masked states (both streams write the same zeros)
+        if (valid < kBN && w.len < p.n_kv) {
+          // the value rows of masked states (both streams write the same zeros)
           const uint32_t uv = u0 + 2 * j + 1;
-          if (ok) ok = wait_all(kv_full[uv % kStages], uv / kStages);
-          zero_rows<Sh::kBlocks>(sKV + (uv % kStages) * kTile, 64 * ch + max(valid, 0),
-                                 64 * ch + 64, threadIdx.x % 128, 128);
+          ok = wait_all(kv_full[uv % kStages], uv / kStages);
+          if (!ok) break;
+          zero_rows<Sh::kBlocks, kBN>(sKV + (uv % kStages) * kKvTile, valid, kBN, row, kBM);
           fence_proxy_async_smem();
         }
-        uint32_t pw[16];
-        l += exp_pairs<Sh::kPolyPairs>(s, p.scale_log2, m, pw);
-        tmem_ld32_wait(ts + 32, s);
-        if constexpr (!Sh::kAliasP) {
-          tc_fence_before();
-          mbar_arrive(smem_u32(&s_free[i]));
-        }
-        tmem_st16(tp, pw);
-        mask_scores(s, valid - 32);
-        l += exp_pairs<Sh::kPolyPairs>(s, p.scale_log2, m, pw);
-        tmem_st16(tp + 16, pw);
+        tmem_st20(tp, pw);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_u32(&p_full[i][ch]));
+        mbar_arrive(smem_u32(&p_full[i][0]));
+        l += exp_pairs(s + kHalf, p.scale_log2, m, pw);
+        tmem_st20(tp + kHalf / 2, pw);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&p_full[i][1]));
       }
-      if (!ok) break;       // (left at the barrier above, by every thread of the stream)
+      if (!ok) break;
       u0 += 2 * w.nt;
       ok = wait_all(pv_done[i], t - 1);
-      tc_fence_after();
-      *mine = l;
-      ok = !named_bar_or(1 + i, kStreamThreads, !ok);
       if (!ok) break;
-      l += *other;
+      tc_fence_after();
       const float inv_l = 1.f / l;
       const int n = w.q0 + i * kBM + row;
-      if (p.lse != nullptr && ch == 0 && n < p.n_q)
+      if (p.lse != nullptr && n < p.n_q)
         p.lse[(static_cast<int64_t>(w.b) * p.H + w.h) * p.n_q + n] = (m + log2f(l)) * kLn2;
       // O / l over the item's Q tile, which its last product has read: 16-byte pieces of this row
       // where a TMA copy with the 128-byte swizzle expects them
       const uint32_t stage = sQ + (2 * i + (n_item & 1)) * kTile;
 #pragma unroll 1
-      for (int c = 0; c < D / 2; c += 32) {
+      for (int c = 0; c < D; c += 32) {
         uint32_t r[32];
         tmem_ld32_wait(to + c, r);
-        const int col = D / 2 * ch + c;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t v[4];
@@ -495,15 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e)
             v[e] = pack_bf16x2(__uint_as_float(r[8 * k + 2 * e]) * inv_l,
                                __uint_as_float(r[8 * k + 2 * e + 1]) * inv_l);
-          store_shared16(swizzled_piece(stage + (col / 64) * kBlk, row, (col % 64) / 8 + k), v);
+          store_shared16(swizzled_piece(stage + (c / 64) * kBlk, row, (c % 64) / 8 + k), v);
         }
       }
       tc_fence_before();
       mbar_arrive(smem_u32(&o_free[i]));
       fence_proxy_async_smem();
       mbar_arrive(smem_u32(&o_staged[i]));
-      // the row sums are read before the next item's maxima take their place
-      named_bar_sync(1 + i, kStreamThreads);
       ++n_item;
     }
   }
