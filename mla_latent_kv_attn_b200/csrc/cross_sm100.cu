@@ -11,15 +11,15 @@
 //                 rounded to bf16 (the tensor cores' operand type; the row sum l is taken from the
 //                 unrounded values in fp32); O / l into shared memory, lse
 //   warp 8        TMA producer: the item's two Q tiles (into the buffer that the item before last
-//                 left), then K_0, V_0, K_1, V_1, ... (80 states each) through a ring of stages
+//                 left), then K_0, V_0, K_1, V_1, ... through a ring of stages
 //   warps 9, 10   MMA issuer of stream 0, 1: S = Q K_j^T (both in shared memory) and
 //                 O += P_j V_j (P in TMEM, V read MN-major)
 //   warp 11       TMA stores of O from the item's Q buffer.  (Stored by the softmax threads, 16
 //                 bytes of 32 rows at a time, O took 9000 cycles an item.)
-// A tile has 80 states: S (80 columns) and P (40) of a stream then fit beside an O of 128, all of TMEM
-// with two streams, and QK(j+1) runs under the softmax of j.  With 128 states P has to take the place
-// of S, and a step is the chain QK, softmax, PV: 4900 cycles a pair of tiles of 128, against 2048 of
-// products.
+// A tile has 128 states for d 64 and 80 for d 128: S (80 columns) and P (40) of a stream then fit
+// beside an O of 128, all of TMEM with two streams, and QK(j+1) runs under the softmax of j.  With 128
+// states P would have to take the place of S, and a step is the chain QK, softmax, PV: 4900 cycles a
+// pair of tiles of 128, against 2048 of products.
 // An item's first QK of stream 1 waits for that of stream 0: streams in step would load the tensor
 // and the CUDA cores in turn (6000 cycles a pair of tiles, against 2048 of products and 4500 as it is).
 // States past a sample's length are masked: their scores become -infinity by selection, and their
@@ -33,8 +33,6 @@ namespace {
 using namespace sm100;
 
 constexpr int kBM = kCrossTile;      // query rows of a stream
-constexpr int kBN = 80;              // states of a tile
-constexpr int kHalf = kBN / 2;
 constexpr int kStreamThreads = 128;
 constexpr int kProducerWarp = 8;
 constexpr int kIssuerWarp = 9;       // and 10; warp 9 also allocates TMEM
@@ -47,6 +45,7 @@ template <int D_>
 struct FwdShape {
   static constexpr int D = D_;
   static_assert(D == 64 || D == 128, "head width");
+  static constexpr int kBN = D == 128 ? 80 : 128;         // states of a tile
   static constexpr int kBlocks = D / 64;                  // 64-column blocks, 128B swizzle
   static constexpr int kBlk = kBM * 128;                  // 16 KB
   static constexpr int kTile = kBlocks * kBlk;            // Q, O
@@ -56,12 +55,11 @@ struct FwdShape {
   static constexpr int kTileBytes = 4 * kTile + kStages * kKvTile;
   static constexpr int kSmem = kTileBytes + 1024;         // tiles, then FwdShared
   static_assert(kSmem <= 227 * 1024, "shared memory");
+  // TMEM columns of stream i
+  static constexpr uint32_t s_col(int i) { return 128u * i; }
+  static constexpr uint32_t p_col(int i) { return D == 128 ? 128u * i + kBN : 256u + 64u * i; }
+  static constexpr uint32_t o_col(int i) { return D == 128 ? 256u + 128u * i : 384u + 64u * i; }
 };
-// TMEM columns of stream i
-__host__ __device__ constexpr uint32_t s_col(int i) { return 128u * i; }
-__host__ __device__ constexpr uint32_t p_col(int i) { return 128u * i + kBN; }
-__host__ __device__ constexpr uint32_t o_col(int i) { return 256u + 128u * i; }
-
 struct CrossFwdParams {
   int n_q, H, rep, n_kv, pairs;      // pairs: items per (sample, head)
   int items;
@@ -95,7 +93,7 @@ struct Item {
 
 // Item `it` (the last one when there is none).  Every role decodes an item ahead of its work: the
 // length comes from global memory, some 700 cycles away.
-__device__ __forceinline__ Item item_of(const CrossFwdParams& p, int it) {
+__device__ __forceinline__ Item item_of(const CrossFwdParams& p, int it, int bn) {
   it = min(it, p.items - 1);
   Item w;
   w.q0 = (it % p.pairs) * 2 * kBM;
@@ -103,11 +101,17 @@ __device__ __forceinline__ Item item_of(const CrossFwdParams& p, int it) {
   w.h = bh % p.H;
   w.b = bh / p.H;
   w.len = cross_len(p.kv_len, w.b, p.n_kv);
-  w.nt = ceil_div(w.len, kBN);
+  w.nt = ceil_div(w.len, bn);
   return w;
 }
 
+__device__ __forceinline__ void load_scores(uint32_t t, uint32_t (&s)[80]) { tmem_ld80_wait(t, s); }
+__device__ __forceinline__ void load_scores(uint32_t t, uint32_t (&s)[128]) { tmem_ld128_wait(t, s); }
+__device__ __forceinline__ void store_pairs(uint32_t t, const uint32_t (&w)[20]) { tmem_st20(t, w); }
+__device__ __forceinline__ void store_pairs(uint32_t t, const uint32_t (&w)[32]) { tmem_st32(t, w); }
+
 // The largest of a row's scores; those from `valid` on become -infinity.
+template <int kBN>
 __device__ __forceinline__ float masked_max(uint32_t (&s)[kBN], int valid) {
   if (valid < kBN) {
 #pragma unroll
@@ -126,13 +130,16 @@ __device__ __forceinline__ float masked_max(uint32_t (&s)[kBN], int valid) {
   return fmaxf(fmax3(fmax3(m8[0], m8[1], m8[2]), m8[3], m8[4]), fmax3(m8[5], m8[6], m8[7]));
 }
 
-// p = 2^(s scale - m) of half of a row's scores, packed to bf16 pairs; returns their sum.
+// p = 2^(s scale - m) of 2 kPairs consecutive scores of a row, packed to bf16 pairs; returns their
+// sum.  (Taking every fourth or more of them from a polynomial on the FMA pipe made the call 4 to 7 %
+// slower.)
+template <int kPairs>
 __device__ __forceinline__ float exp_pairs(const uint32_t* s, float scale_log2, float m,
-                                           uint32_t (&w)[kHalf / 2]) {
+                                           uint32_t (&w)[kPairs]) {
   const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-m, -m);
   uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-  for (int i = 0; i < kHalf / 2; ++i) {
+  for (int i = 0; i < kPairs; ++i) {
     float x0, x1;
     f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, nm2),
               x0, x1);
@@ -153,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tm_o, CrossFwdParams p) {
   using Sh = FwdShape<D>;
   constexpr int kStages = Sh::kStages, kTile = Sh::kTile, kBlk = Sh::kBlk;
-  constexpr int kKvTile = Sh::kKvTile, kKvBlk = Sh::kKvBlk;
+  constexpr int kKvTile = Sh::kKvTile, kKvBlk = Sh::kKvBlk, kBN = Sh::kBN, kHalf = kBN / 2;
   // (the declared alignment is the swizzle's; there is no shared memory beside this)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sQ = smem_u32(smem_raw), sKV = sQ + 4 * kTile;  // Q buffer b of stream i: 2 i + b
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto wait = [&](uint64_t& bar, uint32_t phase) {
     return mbar_wait_or_abort(smem_u32(&bar), phase & 1, abort_flag, p.dev_status);
   };
-  Item next = item_of(p, blockIdx.x);
+  Item next = item_of(p, blockIdx.x, kBN);
 
   if (warp == kProducerWarp) {
     if (lane == 0) {
@@ -218,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
         const Item w = next;
-        next = item_of(p, it + gridDim.x);
+        next = item_of(p, it + gridDim.x, kBN);
         if (w.nt == 0) continue;
         for (int i = 0; i < 2 && ok; ++i) {
           if (w.q0 + i * kBM >= p.n_q) break;
@@ -251,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
         const Item w = next;
-        next = item_of(p, it + gridDim.x);
+        next = item_of(p, it + gridDim.x, kBN);
         if (w.nt == 0) continue;
         for (int i = 0; i < 2; ++i) {
           if (w.q0 + i * kBM >= p.n_q) break;
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t qd0 = smem_desc(sQ + 2 * i * kTile, 16, 1024, kSwizzle128B);
       const uint64_t kd0 = smem_desc(sKV, 16, 1024, kSwizzle128B);
       const uint64_t vd0 = smem_desc(sKV, kKvBlk, 1024, kSwizzle128B);
-      const uint32_t ts = tmem + s_col(i), tp = tmem + p_col(i), to = tmem + o_col(i);
+      const uint32_t ts = tmem + Sh::s_col(i), tp = tmem + Sh::p_col(i), to = tmem + Sh::o_col(i);
       uint32_t n_item = 0, t = 0, u0 = 0;   // items and tiles of this stream, uses of the ring
       uint32_t n_both = 0;                  // items in which both streams have rows
       bool ok = true;
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
         const Item w = next;
-        next = item_of(p, it + gridDim.x);
+        next = item_of(p, it + gridDim.x, kBN);
         if (w.nt == 0) continue;
         if (w.q0 + i * kBM >= p.n_q) {     // no rows for this stream: release what it would read
           for (int j = 0; j < 2 * w.nt && ok; ++j, ++u0) {
@@ -350,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = warp / 4;                              // stream
     const int row = (warp % 4) * 32 + lane;              // TMEM lane
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-    const uint32_t ts = tl + s_col(i), tp = tl + p_col(i), to = tl + o_col(i);
+    const uint32_t ts = tl + Sh::s_col(i), tp = tl + Sh::p_col(i), to = tl + Sh::o_col(i);
     const auto wait_all = [&](uint64_t& bar, uint32_t phase) {
       return __all_sync(0xffffffffu, wait(bar, phase)) != 0;
     };
@@ -358,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
       const Item w = next;
-      next = item_of(p, it + gridDim.x);
+      next = item_of(p, it + gridDim.x, kBN);
       if (w.nt == 0) {
         const int n = w.q0 + i * kBM + row;
         if (n < p.n_q) {
@@ -381,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int valid = w.len - j * kBN;
         uint32_t s[kBN];
-        tmem_ld80_wait(ts, s);
+        load_scores(ts, s);
         tc_fence_before();
         mbar_arrive(smem_u32(&s_free[i]));
         const float mx = masked_max(s, valid) * p.scale_log2;
@@ -422,12 +429,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           zero_rows<Sh::kBlocks, kBN>(sKV + (uv % kStages) * kKvTile, valid, kBN, row, kBM);
           fence_proxy_async_smem();
         }
-        tmem_st20(tp, pw);
+        store_pairs(tp, pw);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(smem_u32(&p_full[i][0]));
         l += exp_pairs(s + kHalf, p.scale_log2, m, pw);
-        tmem_st20(tp + kHalf / 2, pw);
+        store_pairs(tp + kHalf / 2, pw);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(smem_u32(&p_full[i][1]));
@@ -479,8 +486,8 @@ mla_status fwd_impl(const CrossDims& d, const CrossArgs& a, cudaStream_t s) {
   CUtensorMap tq, tk, tv, to;
   mla_status st;
   if ((st = cross_tmap(&tq, a.q, d.B, d.n_q, d.H, D, d.q_row, kBM)) != MLA_OK) return st;
-  if ((st = cross_tmap(&tk, a.k, d.B, d.n_kv, d.Hkv, D, d.k_row, kBN)) != MLA_OK) return st;
-  if ((st = cross_tmap(&tv, a.v, d.B, d.n_kv, d.Hkv, D, d.v_row, kBN)) != MLA_OK) return st;
+  if ((st = cross_tmap(&tk, a.k, d.B, d.n_kv, d.Hkv, D, d.k_row, Sh::kBN)) != MLA_OK) return st;
+  if ((st = cross_tmap(&tv, a.v, d.B, d.n_kv, d.Hkv, D, d.v_row, Sh::kBN)) != MLA_OK) return st;
   if ((st = cross_tmap(&to, a.out, d.B, d.n_q, d.H, D, d.H * D, kBM)) != MLA_OK) return st;
   CrossFwdParams p;
   p.n_q = d.n_q; p.H = d.H; p.rep = d.H / d.Hkv; p.n_kv = d.n_kv;
