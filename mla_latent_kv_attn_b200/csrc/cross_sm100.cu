@@ -38,6 +38,8 @@ constexpr int kProducerWarp = 8;
 constexpr int kIssuerWarp = 9;       // and 10; warp 9 also allocates TMEM
 constexpr int kStoreWarp = 11;
 constexpr int kThreads = 384;
+constexpr int kSms = 148;
+constexpr int kMaxSplits = 8;         // CTAs of a cluster
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -53,16 +55,20 @@ struct FwdShape {
   static constexpr int kKvTile = kBlocks * kKvBlk;
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kTileBytes = 4 * kTile + kStages * kKvTile;
-  static constexpr int kSmem = kTileBytes + 1024;         // tiles, then FwdShared
+  static constexpr int kSmem = kTileBytes + 2048;         // tiles, then FwdShared
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // TMEM columns of stream i
   static constexpr uint32_t s_col(int i) { return 128u * i; }
   static constexpr uint32_t p_col(int i) { return D == 128 ? 128u * i + kBN : 256u + 64u * i; }
   static constexpr uint32_t o_col(int i) { return D == 128 ? 256u + 128u * i : 384u + 64u * i; }
 };
+
 struct CrossFwdParams {
-  int n_q, H, rep, n_kv, pairs;      // pairs: items per (sample, head)
-  int items;
+  int n_q, H, rep, n_kv;
+  // Items: `wide` ones of two query tiles (pairs per sample and head: of its tiles, in order), then
+  // `halves` of one tile each that the pairs from `wide` on fall into, then the odd last tiles.
+  int pairs, wide, halves, items;
+  int splits;                        // CTAs (a cluster) that share an item's states
   float scale_log2;
   const int32_t* kv_len;
   bf16* out;
@@ -84,11 +90,13 @@ struct FwdShared {
   uint64_t first_qk[2];      // stream 0's first S of an item (by parity)
   uint32_t tmem_base;
   int abort_flag;
+  float part_m[kBM], part_l[kBM];      // a split item's share of the row maxima and sums
 };
-static_assert(sizeof(FwdShared<8>) <= 1024, "shared memory");
+static_assert(sizeof(FwdShared<8>) <= 2048, "shared memory");
 
 struct Item {
-  int b, h, q0, len, nt;
+  int b, h, q0, streams, len;
+  int j0, nt;                // first tile of states, and how many
 };
 
 // Item `it` (the last one when there is none).  Every role decodes an item ahead of its work: the
@@ -96,11 +104,27 @@ struct Item {
 __device__ __forceinline__ Item item_of(const CrossFwdParams& p, int it, int bn) {
   it = min(it, p.items - 1);
   Item w;
-  w.q0 = (it % p.pairs) * 2 * kBM;
-  const int bh = it / p.pairs;
+  int bh;
+  if (it < p.wide) {
+    bh = it / p.pairs;
+    w.q0 = (it % p.pairs) * 2 * kBM;
+    w.streams = 2;
+  } else {
+    it -= p.wide;
+    if (it < p.halves) {
+      const int pair = p.wide + it / 2;
+      bh = pair / p.pairs;
+      w.q0 = (pair % p.pairs * 2 + it % 2) * kBM;
+    } else {
+      bh = it - p.halves;
+      w.q0 = p.pairs * 2 * kBM;
+    }
+    w.streams = 1;
+  }
   w.h = bh % p.H;
   w.b = bh / p.H;
   w.len = cross_len(p.kv_len, w.b, p.n_kv);
+  w.j0 = 0;
   w.nt = ceil_div(w.len, bn);
   return w;
 }
@@ -152,7 +176,9 @@ __device__ __forceinline__ float exp_pairs(const uint32_t* s, float scale_log2, 
   return l0 + l1;
 }
 
-template <int D>
+// kSplit: a cluster of p.splits CTAs takes one item of one query tile, each a share of its states;
+// their O, m and l meet in shared memory at the end.
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k,
@@ -179,6 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int* abort_flag = &sh.abort_flag;
 
+  if (kSplit && threadIdx.x < kBM) {
+    sh.part_m[threadIdx.x] = -INFINITY;
+    sh.part_l[threadIdx.x] = 0.f;
+  }
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
     for (int i = 0; i < 2; ++i) {
@@ -214,7 +244,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto wait = [&](uint64_t& bar, uint32_t phase) {
     return mbar_wait_or_abort(smem_u32(&bar), phase & 1, abort_flag, p.dev_status);
   };
-  Item next = item_of(p, blockIdx.x, kBN);
+  const int first_item = kSplit ? blockIdx.x / p.splits : blockIdx.x;
+  const int item_step = kSplit ? p.items : gridDim.x;           // (a cluster has one item)
+  const auto decode = [&](int it) {
+    Item w = item_of(p, it, kBN);
+    if constexpr (kSplit) {
+      const int rank = blockIdx.x % p.splits, nt = w.nt;
+      w.j0 = nt * rank / p.splits;
+      w.nt = nt * (rank + 1) / p.splits - w.j0;
+    }
+    return w;
+  };
+  Item next = decode(first_item);
 
   if (warp == kProducerWarp) {
     if (lane == 0) {
@@ -223,12 +264,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_v);
       uint32_t n_item[2] = {0, 0}, u = 0;          // items of the streams, uses of the ring
       bool ok = true;
-      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+      for (int it = first_item; it < p.items && ok; it += item_step) {
         const Item w = next;
-        next = item_of(p, it + gridDim.x, kBN);
+        next = decode(it + item_step);
         if (w.nt == 0) continue;
-        for (int i = 0; i < 2 && ok; ++i) {
-          if (w.q0 + i * kBM >= p.n_q) break;
+        for (int i = 0; i < w.streams && ok; ++i) {
           const int b = n_item[i] & 1;
           ok = wait(q_empty[i][b], (n_item[i] >> 1) + 1);
           if (!ok) break;
@@ -247,21 +287,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(fb, kKvTile);
           for (int k = 0; k < Sh::kBlocks; ++k)
             tma_load_4d(sKV + s * kKvTile + k * kKvBlk, j & 1 ? &tm_v : &tm_k, fb, 64 * k, w.h / p.rep,
-                        (j >> 1) * kBN, w.b);
+                        (w.j0 + (j >> 1)) * kBN, w.b);
         }
       }
     }
   } else if (warp == kStoreWarp) {
-    if (lane == 0) {
+    if (!kSplit && lane == 0) {
       tma_prefetch_desc(&tm_o);
       uint32_t n_item[2] = {0, 0};
       bool ok = true;
-      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+      for (int it = first_item; it < p.items && ok; it += item_step) {
         const Item w = next;
-        next = item_of(p, it + gridDim.x, kBN);
+        next = decode(it + item_step);
         if (w.nt == 0) continue;
-        for (int i = 0; i < 2; ++i) {
-          if (w.q0 + i * kBM >= p.n_q) break;
+        for (int i = 0; i < w.streams; ++i) {
           ok = wait(o_staged[i], n_item[i]);
           if (!ok) break;
           const int b = n_item[i]++ & 1;
@@ -297,18 +336,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(smem_u32(&kv_empty[u % kStages]));
         mma_commit(smem_u32(&s_full[i]));
       };
-      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+      for (int it = first_item; it < p.items && ok; it += item_step) {
         const Item w = next;
-        next = item_of(p, it + gridDim.x, kBN);
+        next = decode(it + item_step);
         if (w.nt == 0) continue;
-        if (w.q0 + i * kBM >= p.n_q) {     // no rows for this stream: release what it would read
+        if (i >= w.streams) {              // no rows for this stream: release what it would read
           for (int j = 0; j < 2 * w.nt && ok; ++j, ++u0) {
             ok = wait(kv_full[u0 % kStages], u0 / kStages);
             if (ok) mbar_arrive(smem_u32(&kv_empty[u0 % kStages]));
           }
           continue;
         }
-        const bool both = w.q0 + kBM < p.n_q;
+        const bool both = w.streams == 2;
         ok = wait(q_full[i][n_item & 1], n_item >> 1);
         // Stream 0 cannot be two such items ahead of stream 1 (whose Q buffers would have to be
         // free again), so a barrier for each parity tells the items apart.
@@ -363,12 +402,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint32_t t = 0, u0 = 0, n_item = 0;
     bool ok = true;
-    for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+    for (int it = first_item; it < p.items && ok; it += item_step) {
       const Item w = next;
-      next = item_of(p, it + gridDim.x, kBN);
+      next = decode(it + item_step);
       if (w.nt == 0) {
+        if constexpr (kSplit) break;
         const int n = w.q0 + i * kBM + row;
-        if (n < p.n_q) {
+        if (i < w.streams && n < p.n_q) {
           uint4* o4 = reinterpret_cast<uint4*>(
               p.out + ((static_cast<int64_t>(w.b) * p.n_q + n) * p.H + w.h) * D);
           for (int c = 0; c < D / 8; ++c) o4[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -377,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      if (w.q0 + i * kBM >= p.n_q) {
+      if (i >= w.streams) {
         u0 += 2 * w.nt;
         continue;
       }
@@ -386,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_all(s_full[i], t);
         if (!ok) break;
         tc_fence_after();
-        const int valid = w.len - j * kBN;
+        const int valid = w.len - (w.j0 + j) * kBN;
         uint32_t s[kBN];
         load_scores(ts, s);
         tc_fence_before();
@@ -444,6 +484,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait_all(pv_done[i], t - 1);
       if (!ok) break;
       tc_fence_after();
+      if constexpr (kSplit) {
+        // O as it is, 16-byte pieces of a row in an order that spreads them over the banks
+        sh.part_m[row] = m;
+        sh.part_l[row] = l;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t r[16];
+          tmem_ld16_wait(to + c, r);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t v[4] = {r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]};
+            store_shared16(sQ + row * (4 * D) + ((c / 4 + k) ^ (row % (D / 4))) * 16, v);
+          }
+        }
+        break;
+      }
       const float inv_l = 1.f / l;
       const int n = w.q0 + i * kBM + row;
       if (p.lse != nullptr && n < p.n_q)
@@ -478,6 +534,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if constexpr (kSplit) {
+    // Every thread of the cluster comes here, also behind a wait that ran out (its rows then still
+    // say m = -infinity).  O = sum_r 2^(m_r - m) O_r / sum_r 2^(m_r - m) l_r over the CTAs in order;
+    // a thread takes four columns of a row.
+    cluster_sync_all();
+    const Item w = item_of(p, first_item, kBN);
+    const int rows = min(kBM, p.n_q - w.q0);
+    for (int e = (blockIdx.x % p.splits) * kThreads + threadIdx.x; e < rows * (D / 4);
+         e += p.splits * kThreads) {
+      const int r = e / (D / 4), piece = e % (D / 4);
+      const uint32_t at_m = smem_u32(&sh.part_m[r]), at_l = smem_u32(&sh.part_l[r]);
+      const uint32_t at_o = sQ + r * (4 * D) + (piece ^ (r % (D / 4))) * 16;
+      // every load is on its way before the first is used
+      float mc[kMaxSplits], lc[kMaxSplits];
+      float4 oc[kMaxSplits];
+#pragma unroll
+      for (int c = 0; c < kMaxSplits; ++c) {
+        const bool in = c < p.splits;
+        mc[c] = in ? load_cluster_f(map_to_cta(at_m, c)) : -INFINITY;
+        lc[c] = in ? load_cluster_f(map_to_cta(at_l, c)) : 0.f;
+        oc[c] = in ? load_cluster_f4(map_to_cta(at_o, c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float m = mc[0], l = 0.f;
+#pragma unroll
+      for (int c = 1; c < kMaxSplits; ++c) m = fmaxf(m, mc[c]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < kMaxSplits; ++c) {
+        if (mc[c] == -INFINITY) continue;        // no states
+        const float f = fast_exp2(mc[c] - m);
+        l = fmaf(f, lc[c], l);
+        o.x = fmaf(f, oc[c].x, o.x);
+        o.y = fmaf(f, oc[c].y, o.y);
+        o.z = fmaf(f, oc[c].z, o.z);
+        o.w = fmaf(f, oc[c].w, o.w);
+      }
+      const float inv = w.len > 0 ? 1.f / l : 0.f;
+      const int64_t n = w.q0 + r;
+      *reinterpret_cast<uint2*>(p.out + ((w.b * static_cast<int64_t>(p.n_q) + n) * p.H + w.h) * D +
+                                4 * piece) =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      if (piece == 0 && p.lse != nullptr)
+        p.lse[(static_cast<int64_t>(w.b) * p.H + w.h) * p.n_q + n] = (m + log2f(l)) * kLn2;
+    }
+    cluster_sync_all();       // the others have read this CTA's part
+  }
 }
 
 template <int D>
@@ -491,15 +593,46 @@ mla_status fwd_impl(const CrossDims& d, const CrossArgs& a, cudaStream_t s) {
   if ((st = cross_tmap(&to, a.out, d.B, d.n_q, d.H, D, d.H * D, kBM)) != MLA_OK) return st;
   CrossFwdParams p;
   p.n_q = d.n_q; p.H = d.H; p.rep = d.H / d.Hkv; p.n_kv = d.n_kv;
-  p.pairs = ceil_div(d.n_q, 2 * kBM);
-  p.items = p.pairs * d.H * d.B;      // fewer than 2^31: every item has at least one query row
+  // fewer than 2^31 of each: every item has at least one query row
+  const int tiles = ceil_div(d.n_q, kBM), heads = d.B * d.H, odd = tiles % 2 * heads;
+  const int pairs = tiles / 2 * heads;
+  p.pairs = tiles / 2;
+  p.splits = 1;
+  // Whole rounds of the SMs take pairs.  The pairs of the last, partial round become single tiles if
+  // those fit in one round: a tile alone takes two thirds of a pair's time.
+  p.wide = pairs / kSms * kSms;
+  if (2 * (pairs - p.wide) + odd > kSms) p.wide = pairs;
+  p.halves = 2 * (pairs - p.wide);
+  p.items = p.wide + p.halves + odd;
   p.scale_log2 = d.scale * kLog2e;
   p.kv_len = a.kv_len; p.out = static_cast<bf16*>(a.out); p.lse = a.lse;
   p.dev_status = a.dev_status;
-  MLA_CUDA_TRY(cudaFuncSetAttribute(cross_fwd_tc_kernel<D>,
+  // With at least two SMs for every single tile, several share its states.
+  if (p.wide == 0 && 3 * p.items <= kSms)
+    p.splits = std::min(std::min(kMaxSplits, kSms / p.items), ceil_div(d.n_kv, Sh::kBN));
+  if (p.splits > 1) {
+    MLA_CUDA_TRY(cudaFuncSetAttribute(cross_fwd_tc_kernel<D, true>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.items * p.splits);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Sh::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    MLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, cross_fwd_tc_kernel<D, true>, tq, tk, tv, to, p));
+    return MLA_OK;
+  }
+  MLA_CUDA_TRY(cudaFuncSetAttribute(cross_fwd_tc_kernel<D, false>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem));
-  MLA_CUDA_TRY(launch_pdl(cross_fwd_tc_kernel<D>, dim3(std::min(p.items, 148)), dim3(kThreads),
-                          Sh::kSmem, s, tq, tk, tv, to, p));
+  MLA_CUDA_TRY(launch_pdl(cross_fwd_tc_kernel<D, false>, dim3(std::min(p.items, kSms)),
+                          dim3(kThreads), Sh::kSmem, s, tq, tk, tv, to, p));
   return MLA_OK;
 }
 

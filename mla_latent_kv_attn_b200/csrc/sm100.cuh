@@ -443,6 +443,21 @@ __device__ __forceinline__ bool mbar_wait_cluster_or_abort(uint32_t bar, uint32_
   }
 }
 
+// 16 bytes, or 4, of the shared memory of a CTA of the cluster (cluster-window address).
+__device__ __forceinline__ float4 load_cluster_f4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float load_cluster_f(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 // Every thread of both CTAs of the cluster: barrier.cluster arrive (release) + wait (acquire).
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::

@@ -102,6 +102,11 @@ SHAPES = [
     (1, 9, 20, 3, 3, 256, [19]),
     (1, 7, 6, 3, 1, 8, None),
     (1, 640, 384, 1, 1, 128, None),
+    # more query tiles than SMs: whole rounds of pairs, a last round of halves and odd tiles
+    (3, 700, 100, 20, 5, 64, [100, 0, 81]),
+    (2, 600, 170, 40, 40, 128, [169, 170]),
+    (1, 20000, 33, 1, 1, 128, [31]),
+    (1, 300, 80, 60, 60, 64, [80]),
 ]
 
 
