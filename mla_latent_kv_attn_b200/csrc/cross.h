@@ -53,9 +53,6 @@ __device__ __forceinline__ int cross_len(const int32_t* kv_len, int b, int n_kv)
 constexpr int kCrossMaxD = 256;
 mla_status cross_fwd_simt(const CrossDims& d, const CrossArgs& a, cudaStream_t s);
 mla_status cross_bwd_simt(const CrossDims& d, const CrossBwdArgs& a, float* delta, cudaStream_t s);
-// delta[b, h, i] = sum_e d_out[b, i, h, e] out[b, i, h, e], summed in fp32
-mla_status cross_delta(const CrossDims& d, const void* out, const void* d_out, float* delta,
-                       cudaStream_t s);
 
 // Tensor-core kernels: bf16 with d 64 or 128 (cross_sm100.cu, cross_bwd_sm100.cu).
 bool cross_tc_supported(const CrossDims& d);
