@@ -857,7 +857,7 @@ mla_status mla_cache_read_q4(const mla_config* cfg, const uint8_t* codes, const 
   const Dims d = dims_of(*cfg);
   MLA_TRY(check_q4(d, codes, scales));
   MLA_TRY(check_ptr(cache, "cache"));
-  return q4_read(d, codes, scales, d.W * d.tpf, cache, static_cast<cudaStream_t>(stream));
+  return q4_read(d, codes, scales, cache, static_cast<cudaStream_t>(stream));
 }
 
 size_t mla_attention_q4_workspace_bytes(const mla_config* cfg, int32_t n_valid_frames) {

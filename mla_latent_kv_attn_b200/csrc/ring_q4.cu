@@ -17,7 +17,8 @@
 //
 // The bits work out without a table: a float's exponent and top three mantissa bits, rounded up,
 // minus a bias are the scale byte.  All three passes are bound by memory, or by latency where they
-// move a few megabytes: one thread per group, 16- and 8-byte accesses, no shared memory.
+// move a few megabytes: a thread per group or half group, no shared memory, and few
+// instructions a value (no division, no conversion between integers and floats).
 #include <cuda_fp16.h>
 
 #include "kernels.h"
@@ -29,28 +30,63 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kScaleBias = 107 * 8;     // (fp32 exponent bias 127 - 20) on top of 3 mantissa bits
+constexpr float kRound = 12582912.f;    // 1.5 * 2^23: x + this holds the integer nearest x in its low bits
 
 __device__ __forceinline__ float scale_of(uint32_t byte) {
   return __uint_as_float((byte + kScaleBias) << 20);
 }
 
-// Smallest scale byte whose scale is at least r >= 0: the 20 mantissa bits below the third are
-// rounded up by a carry into the bits above; clamped to the range of a byte.
-__device__ __forceinline__ uint32_t scale_byte(float r) {
-  const int b = static_cast<int>((__float_as_uint(r) + 0xFFFFFu) >> 20) - kScaleBias;
-  return static_cast<uint32_t>(min(max(b, 0), 255));
+// Byte of the smallest scale s with 7 s >= mx >= 0 (255 if there is none): the 20 mantissa bits of
+// mx / 7 below the third are rounded up by a carry into the bits above.  The quotient may have been
+// rounded down to a scale that is a hair too small; 7 s is exact and tells.
+__device__ __forceinline__ uint32_t scale_byte(float mx) {
+  const float r = __fdiv_rn(mx, 7.f);
+  int b = static_cast<int>((__float_as_uint(r) + 0xFFFFFu) >> 20) - kScaleBias;
+  b = min(max(b, 0), 255);
+  if (b < 255 && 7.f * scale_of(b) < mx) ++b;
+  return static_cast<uint32_t>(b);
 }
 
-// 16 values of T to or from 16-byte pieces.
-template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&x)[kQ4Group]) {
-  constexpr int kPieces = kQ4Group * sizeof(T) / 16;
+// x / s to the nearest integer, ties to even, within +-7 (a NaN gives 0): a product with 1/s, put
+// right by the exact remainder x - c s.  (A division each would take several times the
+// instructions, and they bound the pass.)  kShort: x has 8 significant bits, so a quotient that is
+// not a tie lies 2^-13 or more from one, beyond the product's error, and only ties can be wrong.
+template <bool kShort>
+__device__ __forceinline__ float nearest_code(float x, float s, float rcp) {
+  x = x == x ? fminf(fmaxf(x, -7.f * s), 7.f * s) : 0.f;
+  const float t = fmaf(x, rcp, kRound);        // kRound + integer
+  float c = t - kRound;
+  const float rem = fmaf(-c, s, x), h = 0.5f * s;
+  const bool odd = (__float_as_uint(t) & 1u) != 0;
+  if ((fabsf(rem) == h && odd) || (!kShort && fabsf(rem) > h)) c += copysignf(1.f, rem);
+  return c;
+}
+
+// Eight codes, each plus 8, in four bits each (the first lowest): four at a time in the low bits of
+// a float.
+template <bool kShort>
+__device__ __forceinline__ uint32_t encode8(const float* x, float s, float rcp) {
+  uint32_t half[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float f = nearest_code<kShort>(x[4 * i + 3], s, rcp);
+#pragma unroll
+    for (int k = 2; k >= 0; --k) f = fmaf(f, 16.f, nearest_code<kShort>(x[4 * i + k], s, rcp));
+    half[i] = __float_as_uint(f + (8388608.f + 8.f * 4369.f));       // 4369 = 1 + 16 + 256 + 4096
+  }
+  return __byte_perm(half[0], half[1], 0x5410);                     // their low 16 bits
+}
+
+// kN values of T from 16-byte pieces.
+template <int kN, typename T>
+__device__ __forceinline__ void load_values(const T* p, float (&x)[kN]) {
+  constexpr int kPieces = kN * sizeof(T) / 16;
   uint4 raw[kPieces];
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) raw[i] = reinterpret_cast<const uint4*>(p)[i];
   const T* t = reinterpret_cast<const T*>(raw);
 #pragma unroll
-  for (int i = 0; i < kQ4Group; ++i) x[i] = Elem<T>::to_f(t[i]);
+  for (int i = 0; i < kN; ++i) x[i] = Elem<T>::to_f(t[i]);
 }
 
 // Values to U: T itself, or fp16 with what lies past its range held at its limits (only a chunk
@@ -67,29 +103,31 @@ struct To<__half> {
   }
 };
 
-template <typename U>
-__device__ __forceinline__ void store16(U* p, const float (&x)[kQ4Group]) {
-  constexpr int kPieces = kQ4Group * sizeof(U) / 16;
+// kN values as U to 16-byte pieces.
+template <int kN, typename U>
+__device__ __forceinline__ void store_values(U* p, const float (&x)[kN]) {
+  constexpr int kPieces = kN * sizeof(U) / 16;
   uint4 raw[kPieces];
   U* t = reinterpret_cast<U*>(raw);
 #pragma unroll
-  for (int i = 0; i < kQ4Group; ++i) t[i] = To<U>::from(x[i]);
+  for (int i = 0; i < kN; ++i) t[i] = To<U>::from(x[i]);
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) reinterpret_cast<uint4*>(p)[i] = raw[i];
 }
 
-// Values of one group: (code - 8) * scale, exact in fp32 and in bf16.
-__device__ __forceinline__ void decode16(uint2 codes, uint32_t byte, float (&x)[kQ4Group]) {
+// Eight values: (code - 8) * scale, exact in fp32 and in bf16.  A code in the low bits of 2^23 is
+// that float plus the code: no conversion, which the SFU would do.
+__device__ __forceinline__ void decode8(uint32_t codes, uint32_t byte, float (&x)[8]) {
   const float s = scale_of(byte);
 #pragma unroll
-  for (int i = 0; i < kQ4Group; ++i) {
-    const uint32_t w = i < 8 ? codes.x : codes.y;
-    x[i] = static_cast<float>(static_cast<int>((w >> (4 * (i & 7))) & 15u) - 8) * s;
-  }
+  for (int i = 0; i < 8; ++i)
+    x[i] = (__uint_as_float(0x4B000000u | ((codes >> (4 * i)) & 15u)) - 8388616.f) * s;
 }
 
-// One thread per group of the chunk: token j of sample b, group g, goes to ring slot
-// (first_frame + j / tpf) mod W.
+// In the append and the preparation gridDim.y samples take turns, and a sample's pieces (fewer than
+// 2^28) are spread over gridDim.x blocks, one per thread at a time: 32-bit index arithmetic.
+
+// Token j of the chunk, group g, goes to ring slot (first_frame + j / tpf) mod W.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     q4_append_kernel(const T* __restrict__ lat, uint8_t* __restrict__ codes,
@@ -97,59 +135,62 @@ __global__ void __launch_bounds__(kThreads)
                      int tpf, int W, int groups, int first_frame) {
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t total = static_cast<int64_t>(B) * n_q * groups;
-  for (int64_t e = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; e < total;
-       e += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int g = static_cast<int>(e % groups);
-    const int64_t bj = e / groups;
-    const int b = static_cast<int>(bj / n_q), j = static_cast<int>(bj % n_q);
-    const int f = first_frame + j / tpf, slot = f % W;
-    float x[kQ4Group];
-    load16(lat + e * kQ4Group, x);
-    float mx = 0.f;
+  const int total = n_q * groups;
+  for (int b = blockIdx.y; b < B; b += gridDim.y) {
+    for (int e = blockIdx.x * kThreads + threadIdx.x; e < total; e += gridDim.x * kThreads) {
+      const int j = e / groups, g = e - j * groups;
+      const int fj = j / tpf, i = j - fj * tpf;
+      const int f = first_frame + fj, slot = f % W;
+      float x[kQ4Group];
+      load_values<kQ4Group>(lat + (static_cast<int64_t>(b) * total + e) * kQ4Group, x);
+      float mx = 0.f;
 #pragma unroll
-    for (int i = 0; i < kQ4Group; ++i) mx = fmaxf(mx, fabsf(x[i]));   // (a NaN is passed over)
-    const uint32_t byte = scale_byte(__fdiv_rn(mx, 7.f));
-    const float s = scale_of(byte);
-    uint2 c = make_uint2(0u, 0u);
-#pragma unroll
-    for (int i = 0; i < kQ4Group; ++i) {
-      // division, not a product with 1/s: a quotient that is a tie must stay one
-      const float r = x[i] == x[i] ? fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -7.f), 7.f) : 0.f;
-      const uint32_t u = static_cast<uint32_t>(static_cast<int>(r) + 8) << (4 * (i & 7));
-      if (i < 8) c.x |= u;
-      else c.y |= u;
+      for (int k = 0; k < kQ4Group; ++k) mx = fmaxf(mx, fabsf(x[k]));   // (a NaN is passed over)
+      const uint32_t byte = scale_byte(mx);
+      const float s = scale_of(byte), rcp = __frcp_rn(s);
+      constexpr bool kShort = sizeof(T) == 2;
+      const uint2 c = make_uint2(encode8<kShort>(x, s, rcp), encode8<kShort>(x + 8, s, rcp));
+      const int64_t to = ((static_cast<int64_t>(b) * W + slot) * tpf + i) * groups + g;
+      reinterpret_cast<uint2*>(codes)[to] = c;
+      scales[to] = static_cast<uint8_t>(byte);
+      if (g == 0 && i == 0) slot_frame[static_cast<int64_t>(b) * W + slot] = f;
     }
-    const int64_t row = (static_cast<int64_t>(b) * W + slot) * tpf + j % tpf;
-    reinterpret_cast<uint2*>(codes)[row * groups + g] = c;
-    scales[row * groups + g] = static_cast<uint8_t>(byte);
-    if (g == 0 && j % tpf == 0) slot_frame[static_cast<int64_t>(b) * W + slot] = f;
   }
 }
 
-// One thread per group: rows [0, rows) of each sample's ring into out [B, rows, 16 groups].
+// Every row of each sample's ring into out, eight values (half a group) at a time: a warp's stores
+// are 512 consecutive bytes of bf16.  Four loads are on their way before the first is used.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     q4_read_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                   T* __restrict__ out, int B, int rows, int ring_rows, int groups) {
+                   T* __restrict__ out, int64_t total) {
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t per = static_cast<int64_t>(rows) * groups;
-  const int64_t total = B * per;
-  for (int64_t e = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; e < total;
-       e += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t src = (e / per) * ring_rows * groups + e % per;
-    float x[kQ4Group];
-    decode16(reinterpret_cast<const uint2*>(codes)[src], scales[src], x);
-    store16(out + e * kQ4Group, x);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t e0 = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; e0 < total;
+       e0 += 4 * step) {
+    uint32_t c[4], s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t e = min(e0 + k * step, total - 1);
+      c[k] = reinterpret_cast<const uint32_t*>(codes)[e];
+      s[k] = scales[e / 2];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (e0 + k * step >= total) break;
+      float x[8];
+      decode8(c[k], s[k], x);
+      store_values<8>(out + (e0 + k * step) * 8, x);
+    }
   }
 }
 
-// What an attention call over the 4-bit ring reads, in one launch and one thread per 16 values:
-//   e < n_ring               content group of ring row r -> ring[b, r, :] (rows ring_width wide; the
+// What an attention call over the 4-bit ring reads, in one launch; piece e of a sample is
+//   e < n_ring               8 content values of ring row r -> ring[b, r, :] (rows ring_width wide; the
 //                            attention takes positional keys from ws)
-//   e < n_ring + n_chunk     content group of chunk row r -> chunk[b, r, :]  (fp16 only)
-//   else                     16 positional values of key-workspace row r: ring slot r decoded, or
+//   e < n_content            8 content values of chunk row r -> chunk[b, r, :]  (fp16 only)
+//   else                     8 positional values of key-workspace row r: ring slot r decoded, or
 //                            chunk token r - nc_pad, rotated at its position and rounded once;
 //                            zeros in the padding rows (the layout of key_workspace_layout)
 // The content is decoded once per call and not inside the attention kernel: there every CTA (one
@@ -164,58 +205,59 @@ __global__ void __launch_bounds__(kThreads)
                       int first_frame, RopeGeom geom, int32_t* dev_status) {
   grid_dep_wait();
   grid_dep_launch();
-  const int groups = D / kQ4Group, cg = d_c / kQ4Group, rg = groups - cg;
-  const int64_t ring_rows = static_cast<int64_t>(W) * geom.tpf;
-  const int64_t n_ring = static_cast<int64_t>(B) * nc * cg;
-  const int64_t n_content = n_ring + (chunk != nullptr ? static_cast<int64_t>(B) * n_q * cg : 0);
-  const int64_t total = n_content + static_cast<int64_t>(B) * rows_ws * rg;
-  for (int64_t e = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; e < total;
-       e += static_cast<int64_t>(gridDim.x) * kThreads) {
-    float x[kQ4Group];
-    if (e < n_ring) {
-      const int g = static_cast<int>(e % cg);
-      const int64_t br = e / cg;
-      const int64_t src = ((br / nc) * ring_rows + br % nc) * groups + g;
-      decode16(reinterpret_cast<const uint2*>(codes)[src], scales[src], x);
-      store16(ring + br * ring_width + g * kQ4Group, x);
-      continue;
-    }
-    if (e < n_content) {
-      const int g = static_cast<int>((e - n_ring) % cg);
-      const int64_t br = (e - n_ring) / cg;
-      load16(chunk_lat + br * D + g * kQ4Group, x);
-      store16(chunk + br * d_c + g * kQ4Group, x);
-      continue;
-    }
-    const int64_t p = e - n_content;
-    const int g = static_cast<int>(p % rg);
-    const int64_t br = p / rg;
-    const int b = static_cast<int>(br / rows_ws), r = static_cast<int>(br % rows_ws);
-    const bool from_ring = r < nc, from_chunk = r >= nc_pad && r - nc_pad < n_q;
-    if (from_ring) {
-      const int64_t src = (b * ring_rows + r) * groups + cg + g;
-      decode16(reinterpret_cast<const uint2*>(codes)[src], scales[src], x);
-    } else if (from_chunk) {
-      load16(chunk_lat + (static_cast<int64_t>(b) * n_q + (r - nc_pad)) * D + d_c + g * kQ4Group, x);
-    } else {
+  // pieces of 8 values per row: all, content, positional
+  const int pieces = D / 8, cp = d_c / 8, rp = pieces - cp;
+  const int n_ring = nc * cp, n_content = n_ring + (chunk != nullptr ? n_q * cp : 0);
+  const int total = n_content + rows_ws * rp;
+  const uint32_t* codes32 = reinterpret_cast<const uint32_t*>(codes);
+  for (int b = blockIdx.y; b < B; b += gridDim.y) {
+    const int64_t ring_row0 = static_cast<int64_t>(b) * W * geom.tpf;
+    for (int e = blockIdx.x * kThreads + threadIdx.x; e < total; e += gridDim.x * kThreads) {
+      float x[8];
+      if (e < n_ring) {
+        const int r = e / cp, g = e - r * cp;
+        const int64_t src = (ring_row0 + r) * pieces + g;
+        decode8(codes32[src], scales[src / 2], x);
+        store_values<8>(ring + (static_cast<int64_t>(b) * nc + r) * ring_width + g * 8, x);
+        continue;
+      }
+      if (e < n_content) {
+        const int r = (e - n_ring) / cp, g = (e - n_ring) - r * cp;
+        const int64_t row = static_cast<int64_t>(b) * n_q + r;
+        load_values<8>(chunk_lat + row * D + g * 8, x);
+        store_values<8>(chunk + row * d_c + g * 8, x);
+        continue;
+      }
+      const int p = e - n_content, r = p / rp, g = p - r * rp;
+      const bool from_ring = r < nc, from_chunk = r >= nc_pad && r - nc_pad < n_q;
+      if (from_ring) {
+        const int64_t src = (ring_row0 + r) * pieces + cp + g;
+        decode8(codes32[src], scales[src / 2], x);
+      } else if (from_chunk) {
+        load_values<8>(chunk_lat + (static_cast<int64_t>(b) * n_q + (r - nc_pad)) * D + d_c + g * 8, x);
+      } else {
 #pragma unroll
-      for (int i = 0; i < kQ4Group; ++i) x[i] = 0.f;
-    }
-    if (from_ring || from_chunk) {
-      int t, h, w;
-      key_position(slot_frame, b, W, geom.tpf, geom.frame_w, nc, first_frame,
-                   from_ring ? r : nc + (r - nc_pad), t, h, w);
-      if (from_ring) debug_check(t >= 0 && t < first_frame && t >= first_frame - W, dev_status);
+        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      }
+      if (from_ring || from_chunk) {
+        int t, h, w;
+        key_position(slot_frame, b, W, geom.tpf, geom.frame_w, nc, first_frame,
+                     from_ring ? r : nc + (r - nc_pad), t, h, w);
+        if (from_ring) debug_check(t >= 0 && t < first_frame && t >= first_frame - W, dev_status);
 #pragma unroll
-      for (int i = 0; i < kQ4Group; i += 2)
-        rope_rotate(x[i], x[i + 1], rope_angle(geom, (g * kQ4Group + i) / 2, t, h, w));
+        for (int i = 0; i < 8; i += 2)
+          rope_rotate(x[i], x[i + 1], rope_angle(geom, (g * 8 + i) / 2, t, h, w));
+      }
+      store_values<8>(ws + (static_cast<int64_t>(b) * rows_ws + r) * (rp * 8) + g * 8, x);
     }
-    store16(ws + br * (rg * kQ4Group) + g * kQ4Group, x);
   }
 }
 
-int blocks_for(int64_t total) {
-  return static_cast<int>(std::min<int64_t>((total + kThreads - 1) / kThreads, 148 * 8));
+// Blocks for B samples of `total` pieces each: up to eight blocks per SM in all.
+dim3 grid_for(int B, int64_t total) {
+  const int y = std::min(B, 65535);
+  const int64_t x = std::min<int64_t>((total + kThreads - 1) / kThreads, std::max(148 * 8 / y, 1));
+  return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
 }
 
 }  // namespace
@@ -223,7 +265,7 @@ int blocks_for(int64_t total) {
 mla_status q4_append(const Dims& d, const void* chunk_lat, uint8_t* codes, uint8_t* scales,
                      int32_t* slot_frame, int first_frame, cudaStream_t s) {
   const int groups = d.D / kQ4Group;
-  const dim3 grid(blocks_for(static_cast<int64_t>(d.B) * d.n_q * groups));
+  const dim3 grid = grid_for(d.B, static_cast<int64_t>(d.n_q) * groups);
   if (d.dtype == MLA_FP32)
     MLA_CUDA_TRY(launch_pdl(q4_append_kernel<float>, grid, dim3(kThreads), 0, s,
                             static_cast<const float*>(chunk_lat), codes, scales, slot_frame, d.B,
@@ -235,17 +277,16 @@ mla_status q4_append(const Dims& d, const void* chunk_lat, uint8_t* codes, uint8
   return MLA_OK;
 }
 
-mla_status q4_read(const Dims& d, const uint8_t* codes, const uint8_t* scales, int rows, void* out,
+mla_status q4_read(const Dims& d, const uint8_t* codes, const uint8_t* scales, void* out,
                    cudaStream_t s) {
-  if (rows == 0) return MLA_OK;
-  const int groups = d.D / kQ4Group;
-  const dim3 grid(blocks_for(static_cast<int64_t>(d.B) * rows * groups));
+  const int64_t total = static_cast<int64_t>(d.B) * d.W * d.tpf * (d.D / 8);
+  const dim3 grid = grid_for(1, total);
   if (d.dtype == MLA_FP32)
     MLA_CUDA_TRY(launch_pdl(q4_read_kernel<float>, grid, dim3(kThreads), 0, s, codes, scales,
-                            static_cast<float*>(out), d.B, rows, d.W * d.tpf, groups));
+                            static_cast<float*>(out), total));
   else
     MLA_CUDA_TRY(launch_pdl(q4_read_kernel<bf16>, grid, dim3(kThreads), 0, s, codes, scales,
-                            static_cast<bf16*>(out), d.B, rows, d.W * d.tpf, groups));
+                            static_cast<bf16*>(out), total));
   return MLA_OK;
 }
 
@@ -259,10 +300,9 @@ mla_status prepare(const Dims& d, const uint8_t* codes, const uint8_t* scales,
   const Q4Workspace w = q4_workspace_layout(d, n_valid, f16);
   char* base = static_cast<char*>(workspace);
   const int64_t rows = static_cast<int64_t>(kw.nc) + (f16 ? d.n_q : 0);
-  const int64_t total = d.B * (rows * (d.d_c / kQ4Group) +
-                               static_cast<int64_t>(kw.rows) * (d.d_rope / kQ4Group));
+  const int64_t total = rows * (d.d_c / 8) + static_cast<int64_t>(kw.rows) * (d.d_rope / 8);
   MLA_CUDA_TRY(launch_pdl(
-      q4_prepare_kernel<T, U>, dim3(blocks_for(total)), dim3(kThreads), 0, s, codes, scales,
+      q4_prepare_kernel<T, U>, grid_for(d.B, total), dim3(kThreads), 0, s, codes, scales,
       static_cast<const T*>(chunk_lat), slot_frame, reinterpret_cast<U*>(base + w.key_bytes),
       f16 ? reinterpret_cast<U*>(base + w.key_bytes + w.ring_bytes) : static_cast<U*>(nullptr),
       reinterpret_cast<U*>(base), d.B, d.W, d.D, d.d_c, f16 ? d.d_c : d.D, d.n_q, kw.nc, kw.nc_pad,

@@ -22,8 +22,8 @@ Q4Workspace q4_workspace_layout(const Dims& d, int n_valid, bool f16);
 // chunk_lat [B, n_q, D] into the slots of frames first_frame .. first_frame + C - 1.
 mla_status q4_append(const Dims& d, const void* chunk_lat, uint8_t* codes, uint8_t* scales,
                      int32_t* slot_frame, int first_frame, cudaStream_t s);
-// The first `rows` rows of every sample's ring as T values, out [B, rows, D].
-mla_status q4_read(const Dims& d, const uint8_t* codes, const uint8_t* scales, int rows, void* out,
+// Every sample's ring as T values, out [B, W * tpf, D].
+mla_status q4_read(const Dims& d, const uint8_t* codes, const uint8_t* scales, void* out,
                    cudaStream_t s);
 // Writes an attention call's workspace (f16 as above).
 mla_status q4_prepare(const Dims& d, const uint8_t* codes, const uint8_t* scales,
