@@ -54,13 +54,16 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None) -> Option
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if (shape is None or t.shape == shape) and (dtype is None or t.dtype is dtype) and \
+            t.is_contiguous():
+        return t.data_ptr()
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t.data_ptr()
+    return t.data_ptr()      # (a list as shape)
 
 
 def _stream(stream) -> Optional[int]:
@@ -332,30 +335,31 @@ def mla_attention_fwd_static_scratch(c: MLAConfigC, q, chunk_lat, cache, slot_fr
 # ---- the latent ring held in 4 bits -----------------------------------------------------------
 
 
-def _q4_ring(c: MLAConfigC, codes, scales):
-    tpf, _, D = _geom(c)
-    rows = (c.batch, c.window_frames * tpf)
-    return (_ptr(codes, "codes", torch.uint8, (*rows, D // 2)),
-            _ptr(scales, "scales", torch.uint8, (*rows, D // 16)))
+def _q4_ring(codes, scales, B: int, rows: int, D: int):
+    return (_ptr(codes, "codes", torch.uint8, (B, rows, D // 2)),
+            _ptr(scales, "scales", torch.uint8, (B, rows, D // 16)))
 
 
 def mla_cache_append_q4(c: MLAConfigC, chunk_lat, codes, scales, slot_frame, first_frame: int,
                         stream=None) -> None:
     tpf, n_q, D = _geom(c)
+    B, W = c.batch, c.window_frames
     st = _lib.lib().mla_cache_append_q4(
-        ctypes.byref(c), _ptr(chunk_lat, "chunk_lat", torch_dtype(c), (c.batch, n_q, D)),
-        *_q4_ring(c, codes, scales),
-        _ptr(slot_frame, "slot_frame", torch.int32, (c.batch, c.window_frames)), first_frame,
-        _stream(stream))
-    _lib.check("mla_cache_append_q4", st)
+        ctypes.byref(c), _ptr(chunk_lat, "chunk_lat", torch_dtype(c), (B, n_q, D)),
+        *_q4_ring(codes, scales, B, W * tpf, D),
+        _ptr(slot_frame, "slot_frame", torch.int32, (B, W)), first_frame, _stream(stream))
+    if st:
+        _lib.check("mla_cache_append_q4", st)
 
 
 def mla_cache_read_q4(c: MLAConfigC, codes, scales, cache, stream=None) -> None:
     tpf, _, D = _geom(c)
+    B, rows = c.batch, c.window_frames * tpf
     st = _lib.lib().mla_cache_read_q4(
-        ctypes.byref(c), *_q4_ring(c, codes, scales),
-        _ptr(cache, "cache", torch_dtype(c), (c.batch, c.window_frames * tpf, D)), _stream(stream))
-    _lib.check("mla_cache_read_q4", st)
+        ctypes.byref(c), *_q4_ring(codes, scales, B, rows, D),
+        _ptr(cache, "cache", torch_dtype(c), (B, rows, D)), _stream(stream))
+    if st:
+        _lib.check("mla_cache_read_q4", st)
 
 
 def mla_attention_q4_workspace_bytes(c: MLAConfigC, n_valid_frames: int) -> int:
@@ -372,7 +376,7 @@ def _attention_q4(fn_name: str, c: MLAConfigC, query, chunk_lat, codes, scales, 
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = getattr(_lib.lib(), fn_name)(
         ctypes.byref(c), *query, _ptr(chunk_lat, "chunk_lat", dt, (B, n_q, D)),
-        *_q4_ring(c, codes, scales),
+        *_q4_ring(codes, scales, B, c.window_frames * tpf, D),
         _ptr(slot_frame, "slot_frame", torch.int32, (B, c.window_frames)), n_valid_frames,
         first_frame, _ptr(w_uv, "w_uv", dt, (H, c.d_head, c.d_c)), _ptr(out, "out", dt, out_shape),
         _ptr(lse, "lse", torch.float32, (B, H, n_q)), _ptr(workspace, "workspace"), ws_bytes,
@@ -442,28 +446,28 @@ def _rows(t: torch.Tensor, name: str, dtype, shape) -> Tuple[int, int]:
     return t.data_ptr(), row
 
 
-def _cross_dtype(cc: MLACrossConfigC) -> torch.dtype:
-    return torch.float32 if cc.dtype == MLA_FP32 else torch.bfloat16
-
-
 def _cross_inputs(cc: MLACrossConfigC, q, k, v, kv_len):
-    dt = _cross_dtype(cc)
-    kv = (cc.batch, cc.n_kv, cc.n_kv_heads, cc.d_head)
-    return (*_rows(q, "q", dt, (cc.batch, cc.n_q, cc.n_heads, cc.d_head)), *_rows(k, "k", dt, kv),
-            *_rows(v, "v", dt, kv), _ptr(kv_len, "kv_len", torch.int32, (cc.batch,)))
+    """The calls' common arguments, then T and the shapes of q and of k (each field of cc is read
+    once: a ctypes field costs as much as a tensor's shape)."""
+    dt = torch.float32 if cc.dtype == MLA_FP32 else torch.bfloat16
+    B, d = cc.batch, cc.d_head
+    rows, kv = (B, cc.n_q, cc.n_heads, d), (B, cc.n_kv, cc.n_kv_heads, d)
+    return (*_rows(q, "q", dt, rows), *_rows(k, "k", dt, kv), *_rows(v, "v", dt, kv),
+            _ptr(kv_len, "kv_len", torch.int32, (B,))), dt, rows, kv
 
 
 def mla_cross_attention_fwd(cc: MLACrossConfigC, q, k, v, out, lse=None, kv_len=None,
                             dev_status=None, stream=None) -> None:
     """Attention of q [B, n_q, H, d] to the first kv_len[b] of an encoder's states k, v
     [B, n_kv, H_kv, d].  q, k and v may be parts of wider rows (see include/mla.h)."""
-    dt = _cross_dtype(cc)
+    inputs, dt, rows, _ = _cross_inputs(cc, q, k, v, kv_len)
+    B, n_q, H, _ = rows
     st = _lib.lib().mla_cross_attention_fwd(
-        ctypes.byref(cc), *_cross_inputs(cc, q, k, v, kv_len),
-        _ptr(out, "out", dt, (cc.batch, cc.n_q, cc.n_heads, cc.d_head)),
-        _ptr(lse, "lse", torch.float32, (cc.batch, cc.n_heads, cc.n_q)),
-        _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
-    _lib.check("mla_cross_attention_fwd", st)
+        ctypes.byref(cc), *inputs, _ptr(out, "out", dt, rows),
+        _ptr(lse, "lse", torch.float32, (B, H, n_q)), _ptr(dev_status, "dev_status", torch.int32),
+        _stream(stream))
+    if st:
+        _lib.check("mla_cross_attention_fwd", st)
 
 
 def mla_cross_attention_bwd_workspace_bytes(cc: MLACrossConfigC) -> int:
@@ -473,14 +477,14 @@ def mla_cross_attention_bwd_workspace_bytes(cc: MLACrossConfigC) -> int:
 def mla_cross_attention_bwd(cc: MLACrossConfigC, q, k, v, out, lse, d_out, d_q, d_k, d_v,
                             workspace, kv_len=None, dev_status=None, stream=None) -> None:
     """Gradients of mla_cross_attention_fwd, given its out and lse (see include/mla.h)."""
-    dt = _cross_dtype(cc)
-    rows = (cc.batch, cc.n_q, cc.n_heads, cc.d_head)
-    kv = (cc.batch, cc.n_kv, cc.n_kv_heads, cc.d_head)
+    inputs, dt, rows, kv = _cross_inputs(cc, q, k, v, kv_len)
+    B, n_q, H, _ = rows
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = _lib.lib().mla_cross_attention_bwd(
-        ctypes.byref(cc), *_cross_inputs(cc, q, k, v, kv_len), _ptr(out, "out", dt, rows),
-        _ptr(lse, "lse", torch.float32, (cc.batch, cc.n_heads, cc.n_q)),
-        _ptr(d_out, "d_out", dt, rows), _ptr(d_q, "d_q", dt, rows), _ptr(d_k, "d_k", dt, kv),
-        _ptr(d_v, "d_v", dt, kv), _ptr(workspace, "workspace"), ws_bytes,
-        _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
-    _lib.check("mla_cross_attention_bwd", st)
+        ctypes.byref(cc), *inputs, _ptr(out, "out", dt, rows),
+        _ptr(lse, "lse", torch.float32, (B, H, n_q)), _ptr(d_out, "d_out", dt, rows),
+        _ptr(d_q, "d_q", dt, rows), _ptr(d_k, "d_k", dt, kv), _ptr(d_v, "d_v", dt, kv),
+        _ptr(workspace, "workspace"), ws_bytes, _ptr(dev_status, "dev_status", torch.int32),
+        _stream(stream))
+    if st:
+        _lib.check("mla_cross_attention_bwd", st)

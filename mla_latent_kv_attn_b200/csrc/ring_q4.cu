@@ -253,10 +253,10 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Blocks for B samples of `total` pieces each: up to eight blocks per SM in all.
+// Blocks for B samples of `total` pieces each: up to sixteen blocks per SM in all.
 dim3 grid_for(int B, int64_t total) {
   const int y = std::min(B, 65535);
-  const int64_t x = std::min<int64_t>((total + kThreads - 1) / kThreads, std::max(148 * 8 / y, 1));
+  const int64_t x = std::min<int64_t>((total + kThreads - 1) / kThreads, std::max(148 * 16 / y, 1));
   return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
 }
 
