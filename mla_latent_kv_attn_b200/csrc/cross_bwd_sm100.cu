@@ -12,9 +12,8 @@
 // S and dP are computed twice (7 products where 5 would do): a single pass would have to add dQ
 // over blocks, in an order that changes from run to run or in fp32 copies that cost more memory
 // traffic than the two products (115 MB for 4680 queries, 12 heads and 512 states).
-// P and dS are rounded to bf16 as operands; every product accumulates in fp32 in TMEM, where P and
-// dS also take the place of S and dP: a thread that has read 64 columns of scores writes 32 columns
-// of bf16 pairs over them.  Every wait is bounded; one that runs out writes MLA_ERR_DEVICE_TIMEOUT
+// P and dS are rounded to bf16 as operands (in TMEM); every product accumulates in fp32 in TMEM.
+// Every wait is bounded; one that runs out writes MLA_ERR_DEVICE_TIMEOUT
 // to dev_status.
 #include "cross_tc.cuh"
 
@@ -31,12 +30,12 @@ constexpr int kIssuerA = 9, kIssuerB = 10;
 constexpr int kStoreWarp = 11;
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kPolyPairs = 2;             // pairs of 8 whose exponential comes from the polynomial
 
 struct CrossBwdParams {
-  int B, H, Hkv, rep, n_q, n_kv, n_pad;   // n_pad: n_q rounded up to whole tiles
+  int B, H, Hkv, rep, n_q, n_kv, n_pad;   // n_pad: n_q rounded up to whole tiles of both kinds
   int q_tiles, items;                     // dQ: items of one query tile
-  int kv_tiles, splits;                   // dK, dV: blocks that share a tile's queries
+  int kv_tiles, splits;                   // dK, dV: blocks that share a tile's queries,
+  int qn_tiles;                           // query tiles of 80
   float scale, scale_log2;
   const int32_t* kv_len;
   const float* lse2;                      // [B, H, n_pad]
@@ -45,32 +44,29 @@ struct CrossBwdParams {
   int32_t* dev_status;
 };
 
-// p = 2^(s scale - l) of 32 columns of a row whose l is the same (dQ) or that of the column (dK, dV,
-// l2 then holds 16 pairs); kPoly: some exponentials by the polynomial.
-template <bool kPoly>
-__device__ __forceinline__ void probabilities(const uint32_t (&s)[32], uint64_t scale2,
+// p = 2^(s scale - l) of kN columns of a row whose l is the same (dQ, l_step 0) or that of the column
+// (dK, dV: neg_l2 holds kN / 2 pairs).
+template <int kN>
+__device__ __forceinline__ void probabilities(const uint32_t (&s)[kN], uint64_t scale2,
                                               const uint64_t* neg_l2, int l_step, float* p) {
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
+  for (int k = 0; k < kN / 2; ++k) {
     float x0, x1;
     f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), scale2,
                      neg_l2[k * l_step]),
               x0, x1);
-    if (kPoly && (k & 7) < kPolyPairs) {
-      exp2_poly_pair(x0, x1, p[2 * k], p[2 * k + 1]);
-    } else {
-      p[2 * k] = fast_exp2(x0);
-      p[2 * k + 1] = fast_exp2(x1);
-    }
+    p[2 * k] = fast_exp2(x0);
+    p[2 * k + 1] = fast_exp2(x1);
   }
 }
 
-// dS = p (dP scale - delta scale) of 32 columns, as bf16 pairs.
-__device__ __forceinline__ void score_gradients(const uint32_t (&dp)[32], const float* p,
+// dS = p (dP scale - delta scale) of kN columns, as bf16 pairs.
+template <int kN>
+__device__ __forceinline__ void score_gradients(const uint32_t (&dp)[kN], const float* p,
                                                 uint64_t scale2, const uint64_t* neg_d2, int d_step,
-                                                uint32_t (&w)[16]) {
+                                                uint32_t (&w)[kN / 2]) {
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
+  for (int k = 0; k < kN / 2; ++k) {
     float d0, d1;
     f2_unpack(f2_mul(f2_fma(f2_pack(__uint_as_float(dp[2 * k]), __uint_as_float(dp[2 * k + 1])),
                             scale2, neg_d2[k * d_step]),
@@ -93,26 +89,37 @@ __device__ __forceinline__ void mma_pairs_by_tile(uint32_t acc, uint32_t a, uint
            (accumulate || kk) ? 1u : 0u);
 }
 
-// d = A B^T of two K-major tiles [128, D] in shared memory.
-template <int D>
+// d = A B^T of two K-major tiles in shared memory, A [128, D] and B [kN, D].
+template <int D, int kN = kT>
 __device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a_tile, uint32_t b_tile) {
-  constexpr uint32_t idesc = idesc_bf16_f32(kT, kT, 0, 0);
+  constexpr uint32_t idesc = idesc_bf16_f32(kT, kN, 0, 0);
   const uint64_t a = smem_desc(a_tile, 16, 1024, kSwizzle128B);
   const uint64_t b = smem_desc(b_tile, 16, 1024, kSwizzle128B);
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = ((kk >> 2) * kT * 128 >> 4) + 2 * (kk & 3);
-    mma_ss(d, a + off, b + off, idesc, kk ? 1u : 0u);
-  }
+  for (int kk = 0; kk < D / 16; ++kk)
+    mma_ss(d, a + (((kk >> 2) * kT * 128 >> 4) + 2 * (kk & 3)),
+           b + (((kk >> 2) * kN * 128 >> 4) + 2 * (kk & 3)), idesc, kk ? 1u : 0u);
 }
 
-// One thread: the tile of rows [row, row + 128) of head h of sample b.
-template <int D>
+// acc (+)= A B with A [128, kN] as bf16 pairs in kN / 2 columns of TMEM from `a` on, and B [kN, D] a
+// tile read MN-major.
+template <int D, int kN>
+__device__ __forceinline__ void mma_pairs_by_rows(uint32_t acc, uint32_t a, uint32_t tile,
+                                                  bool accumulate) {
+  constexpr uint32_t idesc = idesc_bf16_f32(kT, D, 0, 1);
+  const uint64_t b = smem_desc(tile, kN * 128, 1024, kSwizzle128B);
+#pragma unroll
+  for (int kk = 0; kk < kN / 16; ++kk)
+    mma_ts(acc, a + 8 * kk, b + 128 * kk, idesc, (accumulate || kk) ? 1u : 0u);
+}
+
+// One thread: the tile of rows [row, row + kN) of head h of sample b.
+template <int D, int kN = kT>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int h,
                                           int row, int b) {
 #pragma unroll
   for (int k = 0; k < D / 64; ++k)
-    tma_load_4d(dst + k * kT * 128, map, bar, 64 * k, h, row, b);
+    tma_load_4d(dst + k * kN * 128, map, bar, 64 * k, h, row, b);
 }
 
 // ------------------------------------------------------------------------------------- stats
@@ -420,11 +427,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
           uint32_t s[32];
           tmem_ld32_wait(ts, s);
-          probabilities<true>(s, sl2, &nl2, 0, pr);
+          probabilities<32>(s, sl2, &nl2, 0, pr);
           tmem_ld32_wait(ts + 32, s);
           tc_fence_before();
           mbar_arrive(smem_u32(&sh.s_free));
-          probabilities<true>(s, sl2, &nl2, 0, pr + 32);
+          probabilities<32>(s, sl2, &nl2, 0, pr + 32);
         }
         ok = wait_all(sh.dp_full[t & 1], t >> 1);
         if (!ok) break;
@@ -434,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 64; c += 32) {
           uint32_t dp[32], ds[16];
           tmem_ld32_wait(td + c, dp);
-          score_gradients(dp, pr + c, sc2, &nd2, 0, ds);
+          score_gradients<32>(dp, pr + c, sc2, &nd2, 0, ds);
           if (valid < c + 32) {
             // masked states, whatever their scores and dP hold
 #pragma unroll
@@ -491,38 +498,47 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------------------------- dK, dV
 
+constexpr int kQN = 80;            // queries of a streamed tile (64: the call 4 % slower)
+constexpr int kQH = kQN / 2;       // columns that a thread holds at a time
+
 template <int D_>
 struct DkvShape {
   static constexpr int D = D_;
-  static constexpr int kTile = kT * D * 2;
-  static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr int kTiles = 2 + 2 * kStages;              // K, V, then Q and G of each stage
-  static constexpr int kStatBytes = 2 * kT * 4;               // lse2 and delta of a query tile
-  static constexpr int kSmem = kTiles * kTile + kStages * kStatBytes + 1024;
-  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static constexpr int kTile = kT * D * 2;                    // K, V
+  static constexpr int kQTile = kQN * D * 2;                  // Q_i, G_i
+  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kStatBytes = 2 * kQN * 4;              // lse2 and delta of a query tile
+  static constexpr int kStat = 2 * kTile + 2 * kStages * kQTile;
+  static constexpr int kSync = kStat + kStages * kStatBytes;
+  static constexpr int kSmem = kSync + 1024;
+  static_assert(kSync % 8 == 0 && kSmem <= 227 * 1024, "shared memory");
 };
-constexpr uint32_t kColS = 0, kColDP = 128, kColDK = 256, kColDV = 384;
+// TMEM columns: dK and dV (D each) from 0, then
+constexpr uint32_t kColS = 256, kColP = kColS + kQN, kColDP = 384, kColDS = kColDP + kQN;
 
+// Arrays of two: by the parity of the tile.
 template <int kStages>
 struct DkvShared {
   uint64_t k_full, v_full;
   uint64_t q_full[kStages], q_empty[kStages];    // Q_i and its statistics
   uint64_t g_full[kStages], g_empty[kStages];
-  uint64_t s_full, dp_full;        // S^T, dP^T complete
-  uint64_t p_full, ds_full;        // P^T, dS^T in TMEM
-  uint64_t dv_done, dk_done;       // the products that read them complete
+  uint64_t s_full[2], s_free[2];                 // S^T complete; read
+  uint64_t dp_full[2], dp_free[2];               // dP^T complete; read
+  uint64_t p_full[2], ds_full[2];                // P^T, dS^T in TMEM
+  uint64_t dv_done[2], dk_done[2];               // the products that read them complete
   uint32_t tmem_base;
   int abort_flag;
 };
 
-// A block per split, state tile, key head and sample.  Roles (320 threads): warps 0-7 softmax, 8 TMA
-// producer, 9 issuer.  S^T(i+1) may run once dV(i) has read P^T(i), which the softmax writes before
-// it turns to dS: while dS(i) is being computed the tensor cores have dV(i) and S^T(i+1), and while
-// P(i+1) is, dK(i) and dP^T(i+1).  The step is bound by the chain P, dV, S^T, so one thread issues
-// in that order (two threads, one per pair, interleaved dK with S^T: 3600 cycles a step against
-// 2048 of products).
+// A block per split, state tile, key head and sample.  Roles (352 threads): warps 0-3 and 4-7 softmax
+// of the even and of the odd query tiles, one state (TMEM lane) per thread, 8 TMA producer, 9 issuer
+// of S^T and dV, 10 issuer of dP^T and dK.  With tiles of 80 queries S^T, P^T, dP^T and dS^T have
+// columns of their own beside dK and dV, so every product runs as soon as its operands are there and
+// two tiles are in the softmax at a time.  (With 128 queries P^T has to take the place of S^T and
+// dS^T that of dP^T, and a step is a chain of products and exponentials: 3240 cycles for 128 queries,
+// against 2048 of products.)
 // Rows of masked states hold whatever their scores gave; they reach no other row and are not used.
-constexpr int kThreadsKV = 320;
+constexpr int kThreadsKV = 352;
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsKV, 1)
@@ -531,13 +547,13 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                         const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, CrossBwdParams p) {
   using Sh = DkvShape<D>;
-  constexpr int kTile = Sh::kTile, kStages = Sh::kStages;
+  constexpr int kTile = Sh::kTile, kQTile = Sh::kQTile, kStages = Sh::kStages;
+  constexpr uint32_t kColDK = 0, kColDV = D;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sK = smem_u32(smem_raw), sV = sK + kTile, sQ = sV + kTile;
-  const uint32_t sG = sQ + kStages * kTile, sStat = sG + kStages * kTile;
-  const float* stats = reinterpret_cast<const float*>(smem_raw + Sh::kTiles * kTile);
-  auto& sh = *reinterpret_cast<DkvShared<kStages>*>(smem_raw + Sh::kTiles * kTile +
-                                                    kStages * Sh::kStatBytes);
+  const uint32_t sG = sQ + kStages * kQTile, sStat = sK + Sh::kStat;
+  const float* stats = reinterpret_cast<const float*>(smem_raw + Sh::kStat);
+  auto& sh = *reinterpret_cast<DkvShared<kStages>*>(smem_raw + Sh::kSync);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int split = blockIdx.x % p.splits, bt = blockIdx.x / p.splits;
   const int tile = bt % p.kv_tiles, kh = bt / p.kv_tiles % p.Hkv, b = bt / p.kv_tiles / p.Hkv;
@@ -551,14 +567,18 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
       mbar_init(smem_u32(&sh.q_full[s]), 1);
       mbar_init(smem_u32(&sh.q_empty[s]), 1);
       mbar_init(smem_u32(&sh.g_full[s]), 1);
-      mbar_init(smem_u32(&sh.g_empty[s]), 1);
+      mbar_init(smem_u32(&sh.g_empty[s]), 2);      // dP^T and dV
     }
-    mbar_init(smem_u32(&sh.s_full), 1);
-    mbar_init(smem_u32(&sh.dp_full), 1);
-    mbar_init(smem_u32(&sh.p_full), kSoftmaxThreads);
-    mbar_init(smem_u32(&sh.ds_full), kSoftmaxThreads);
-    mbar_init(smem_u32(&sh.dv_done), 1);
-    mbar_init(smem_u32(&sh.dk_done), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.s_full[i]), 1);
+      mbar_init(smem_u32(&sh.s_free[i]), kT);
+      mbar_init(smem_u32(&sh.dp_full[i]), 1);
+      mbar_init(smem_u32(&sh.dp_free[i]), kT);
+      mbar_init(smem_u32(&sh.p_full[i]), kT);
+      mbar_init(smem_u32(&sh.ds_full[i]), kT);
+      mbar_init(smem_u32(&sh.dv_done[i]), 1);
+      mbar_init(smem_u32(&sh.dk_done[i]), 1);
+    }
     fence_barrier_init();
   }
   if (warp == kIssuerA) {
@@ -575,9 +595,10 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
   const auto wait = [&](uint64_t& bar, uint32_t phase) {
     return mbar_wait_or_abort(smem_u32(&bar), phase & 1, abort_flag, p.dev_status);
   };
+  const auto wait2 = [&](uint64_t (&bar)[2], int i) { return wait(bar[i & 1], i >> 1); };
   const int len = cross_len(p.kv_len, b, p.n_kv);
   // this block's share of the (head, query tile) pairs: none for a tile of masked states
-  const int work = p.rep * p.q_tiles;
+  const int work = p.rep * p.qn_tiles;
   const int first = static_cast<int>(static_cast<int64_t>(work) * split / p.splits);
   const int n = tile * kT < len
                     ? static_cast<int>(static_cast<int64_t>(work) * (split + 1) / p.splits) - first
@@ -593,16 +614,16 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
       bool ok = true;
       for (int i = 0; i < n && ok; ++i) {
         const int s = i % kStages;
-        const int h = kh * p.rep + (first + i) / p.q_tiles, q0 = (first + i) % p.q_tiles * kT;
+        const int h = kh * p.rep + (first + i) / p.qn_tiles, q0 = (first + i) % p.qn_tiles * kQN;
         ok = wait(sh.q_empty[s], i / kStages + 1);
         if (!ok) break;
         const uint32_t qb = smem_u32(&sh.q_full[s]);
         const uint32_t st = sStat + s * Sh::kStatBytes;
         const int64_t so = (static_cast<int64_t>(b) * p.H + h) * p.n_pad + q0;
-        mbar_arrive_expect_tx(qb, kTile + Sh::kStatBytes);
-        load_tile<D>(sQ + s * kTile, &tm_q, qb, h, q0, b);
-        bulk_load(st, p.lse2 + so, kT * 4, qb);
-        bulk_load(st + kT * 4, p.delta + so, kT * 4, qb);
+        mbar_arrive_expect_tx(qb, kQTile + Sh::kStatBytes);
+        load_tile<D, kQN>(sQ + s * kQTile, &tm_q, qb, h, q0, b);
+        bulk_load(st, p.lse2 + so, kQN * 4, qb);
+        bulk_load(st + kQN * 4, p.delta + so, kQN * 4, qb);
         if (i == 0) {
           mbar_arrive_expect_tx(vb, kTile);
           load_tile<D>(sV, &tm_v, vb, kh, tile * kT, b);
@@ -610,111 +631,132 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
         ok = wait(sh.g_empty[s], i / kStages + 1);
         if (!ok) break;
         const uint32_t gb = smem_u32(&sh.g_full[s]);
-        mbar_arrive_expect_tx(gb, kTile);
-        load_tile<D>(sG + s * kTile, &tm_g, gb, h, q0, b);
+        mbar_arrive_expect_tx(gb, kQTile);
+        load_tile<D, kQN>(sG + s * kQTile, &tm_g, gb, h, q0, b);
       }
     }
   } else if (warp == kIssuerA) {
     if (lane == 0) {
-      bool ok = wait(sh.k_full, 0);
       const auto issue_s = [&](int i) {
         const int s = i % kStages;
-        if (!wait(sh.q_full[s], i / kStages)) return false;
+        if (!wait(sh.q_full[s], i / kStages) || (i > 0 && !wait2(sh.s_free, i - 1))) return false;
         tc_fence_after();
-        mma_tiles<D>(tmem + kColS, sK, sQ + s * kTile);
-        mma_commit(smem_u32(&sh.s_full));
+        mma_tiles<D, kQN>(tmem + kColS, sK, sQ + s * kQTile);
+        mma_commit(smem_u32(&sh.s_full[i & 1]));
         return true;
       };
-      const auto issue_dp = [&](int i) {
-        const int s = i % kStages;
-        if (!wait(sh.g_full[s], i / kStages)) return false;
-        tc_fence_after();
-        mma_tiles<D>(tmem + kColDP, sV, sG + s * kTile);
-        mma_commit(smem_u32(&sh.dp_full));
-        return true;
-      };
-      ok = ok && issue_s(0) && wait(sh.v_full, 0) && issue_dp(0);
+      bool ok = wait(sh.k_full, 0) && issue_s(0);
       for (int i = 0; i < n && ok; ++i) {
         const int s = i % kStages;
-        ok = wait(sh.p_full, i);
+        ok = (i + 1 == n || issue_s(i + 1)) && wait(sh.g_full[s], i / kStages) &&
+             wait2(sh.p_full, i);
         if (!ok) break;
         tc_fence_after();
-        mma_pairs_by_tile<D>(tmem + kColDV, tmem + kColS, sG + s * kTile, i > 0);
+        mma_pairs_by_rows<D, kQN>(tmem + kColDV, tmem + kColP, sG + s * kQTile, i > 0);
         mma_commit(smem_u32(&sh.g_empty[s]));
-        mma_commit(smem_u32(&sh.dv_done));
-        ok = i + 1 == n || (wait(sh.dv_done, i) && issue_s(i + 1));
-        ok = ok && wait(sh.ds_full, i);
+        mma_commit(smem_u32(&sh.dv_done[i & 1]));
+      }
+    }
+  } else if (warp == kIssuerB) {
+    if (lane == 0) {
+      const auto issue_dp = [&](int i) {
+        const int s = i % kStages;
+        if (!wait(sh.g_full[s], i / kStages) || (i > 0 && !wait2(sh.dp_free, i - 1))) return false;
+        tc_fence_after();
+        mma_tiles<D, kQN>(tmem + kColDP, sV, sG + s * kQTile);
+        mma_commit(smem_u32(&sh.g_empty[s]));
+        mma_commit(smem_u32(&sh.dp_full[i & 1]));
+        return true;
+      };
+      bool ok = wait(sh.v_full, 0) && issue_dp(0);
+      for (int i = 0; i < n && ok; ++i) {
+        const int s = i % kStages;
+        ok = (i + 1 == n || issue_dp(i + 1)) && wait2(sh.ds_full, i);
         if (!ok) break;
         tc_fence_after();
-        mma_pairs_by_tile<D>(tmem + kColDK, tmem + kColDP, sQ + s * kTile, i > 0);
+        mma_pairs_by_rows<D, kQN>(tmem + kColDK, tmem + kColDS, sQ + s * kQTile, i > 0);
         mma_commit(smem_u32(&sh.q_empty[s]));
-        mma_commit(smem_u32(&sh.dk_done));
-        ok = i + 1 == n || (wait(sh.dk_done, i) && issue_dp(i + 1));
+        mma_commit(smem_u32(&sh.dk_done[i & 1]));
       }
     }
   } else {
-    const int ch = warp / 4, row = (warp % 4) * 32 + lane;
+    const int grp = warp / 4, row = (warp % 4) * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-    const uint32_t ts = tl + kColS + 64 * ch, td = tl + kColDP + 64 * ch;
     // a single state's softmax is constant: its dS is zero
     const float sc = len == 1 ? 0.f : p.scale;
     const uint64_t sl2 = f2_pack(p.scale_log2, p.scale_log2), sc2 = f2_pack(sc, sc);
     const uint64_t neg2 = f2_pack(-1.f, -1.f), nsc2 = f2_pack(-sc, -sc);
-    const auto wait_all = [&](uint64_t& bar, uint32_t phase) {
-      return __all_sync(0xffffffffu, wait(bar, phase)) != 0;
-    };
+    const auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
     bool ok = true;
-    for (int i = 0; i < n; ++i) {
+    for (int i = grp; i < n; i += 2) {
       const int s = i % kStages;
-      // (the statistics came with the loads of q_full)
-      ok = wait_all(sh.q_full[s], i / kStages) && wait_all(sh.s_full, i);
+      // S^T(i); the statistics came with the loads of q_full, complete since
+      ok = all(wait2(sh.s_full, i) && wait(sh.q_full[s], i / kStages));
       if (!ok) break;
       tc_fence_after();
-      const float4* lse4 =
-          reinterpret_cast<const float4*>(stats + s * (Sh::kStatBytes / 4) + 64 * ch);
-      const float4* del4 = lse4 + kT / 4;
-      float pr[64];
+      const float4* lse4 = reinterpret_cast<const float4*>(stats + s * (Sh::kStatBytes / 4));
+      const float4* del4 = lse4 + kQN / 4;
+      float pr[kQN];
+      uint32_t w[2][kQH / 2];
 #pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        uint32_t sc32[32], pw[16];
-        uint64_t nl2[16];
-        tmem_ld32_wait(ts + c, sc32);
+      for (int c = 0; c < kQN; c += kQH) {
+        uint32_t raw[kQH];
+        uint64_t nl2[kQH / 2];
+        tmem_ld40_wait(tl + kColS + c, raw);
+        if (c + kQH == kQN) {
+          tc_fence_before();
+          mbar_arrive(smem_u32(&sh.s_free[i & 1]));
+        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kQH / 4; ++k) {
           const float4 l = lse4[c / 4 + k];
           nl2[2 * k] = f2_mul(f2_pack(l.x, l.y), neg2);
           nl2[2 * k + 1] = f2_mul(f2_pack(l.z, l.w), neg2);
         }
-        probabilities<true>(sc32, sl2, nl2, 1, pr + c);
+        probabilities<kQH>(raw, sl2, nl2, 1, pr + c);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) pw[k] = pack_bf16x2(pr[c + 2 * k], pr[c + 2 * k + 1]);
-        tmem_st16(ts + c / 2, pw);
+        for (int k = 0; k < kQH / 2; ++k) w[c / kQH][k] = pack_bf16x2(pr[c + 2 * k], pr[c + 2 * k + 1]);
       }
+      // dV(i-1) has read P^T(i-1)
+      if (i > 0) ok = all(wait2(sh.dv_done, i - 1));
+      if (!ok) break;
+      tc_fence_after();
+      tmem_st20(tl + kColP, w[0]);
+      tmem_st20(tl + kColP + kQH / 2, w[1]);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(smem_u32(&sh.p_full));
-      ok = wait_all(sh.dp_full, i);
+      mbar_arrive(smem_u32(&sh.p_full[i & 1]));
+      ok = all(wait2(sh.dp_full, i));
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        uint32_t dp[32], ds[16];
-        uint64_t nd2[16];
-        tmem_ld32_wait(td + c, dp);
+      for (int c = 0; c < kQN; c += kQH) {
+        uint32_t dp[kQH];
+        uint64_t nd2[kQH / 2];
+        tmem_ld40_wait(tl + kColDP + c, dp);
+        if (c + kQH == kQN) {
+          tc_fence_before();
+          mbar_arrive(smem_u32(&sh.dp_free[i & 1]));
+        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kQH / 4; ++k) {
           const float4 d = del4[c / 4 + k];
           nd2[2 * k] = f2_mul(f2_pack(d.x, d.y), nsc2);
           nd2[2 * k + 1] = f2_mul(f2_pack(d.z, d.w), nsc2);
         }
-        score_gradients(dp, pr + c, sc2, nd2, 1, ds);
-        tmem_st16(td + c / 2, ds);
+        score_gradients<kQH>(dp, pr + c, sc2, nd2, 1, w[c / kQH]);
       }
+      // dK(i-1) has read dS^T(i-1)
+      if (i > 0) ok = all(wait2(sh.dk_done, i - 1));
+      if (!ok) break;
+      tc_fence_after();
+      tmem_st20(tl + kColDS, w[0]);
+      tmem_st20(tl + kColDS + kQH / 2, w[1]);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(smem_u32(&sh.ds_full));
+      mbar_arrive(smem_u32(&sh.ds_full[i & 1]));
     }
-    if (ok) ok = wait_all(sh.dv_done, n - 1) && wait_all(sh.dk_done, n - 1);
+    if (ok) ok = all(wait2(sh.dv_done, n - 1) && wait2(sh.dk_done, n - 1));
     if (ok) {
       tc_fence_after();
       // four columns of 32 rows are 512 consecutive bytes
@@ -724,8 +766,8 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t r[32];
-        tmem_ld32_wait(tl + (ch == 0 ? kColDK : kColDV) + c, r);
-        float4* dst = reinterpret_cast<float4*>(p.partial + ch * half + tile_at) + (c / 4) * kT + row;
+        tmem_ld32_wait(tl + (grp == 0 ? kColDK : kColDV) + c, r);
+        float4* dst = reinterpret_cast<float4*>(p.partial + grp * half + tile_at) + (c / 4) * kT + row;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           dst[k * kT] = make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
@@ -797,16 +839,18 @@ int dkv_splits(int tiles, int work) {
 }
 
 struct BwdLayout {
-  int n_pad, kv_tiles, splits;
+  int n_pad, q_tiles, qn_tiles, kv_tiles, splits;
   size_t lse2, delta, partial, bytes;      // offsets of the three arrays, and their end
 };
 
 BwdLayout bwd_layout(const CrossDims& d) {
   BwdLayout l;
-  l.n_pad = round_up(d.n_q, kT);
+  l.q_tiles = ceil_div(d.n_q, kT);
+  l.qn_tiles = ceil_div(d.n_q, kQN);
+  l.n_pad = round_up(std::max(l.q_tiles * kT, l.qn_tiles * kQN), kStatRows);
   l.kv_tiles = ceil_div(d.n_kv, kT);
-  l.splits = dkv_splits(d.B * d.Hkv * l.kv_tiles, d.H / d.Hkv * (l.n_pad / kT));
-  const size_t stat = static_cast<size_t>(d.B) * d.H * l.n_pad * sizeof(float);   // 512-byte rows
+  l.splits = dkv_splits(d.B * d.Hkv * l.kv_tiles, d.H / d.Hkv * l.qn_tiles);
+  const size_t stat = static_cast<size_t>(d.B) * d.H * l.n_pad * sizeof(float);   // 256-byte rows
   l.lse2 = 0;
   l.delta = stat;
   l.partial = 2 * stat;
@@ -819,17 +863,19 @@ template <int D>
 mla_status bwd_impl(const CrossDims& d, const CrossBwdArgs& a, void* workspace, cudaStream_t s) {
   const BwdLayout l = bwd_layout(d);
   char* ws = static_cast<char*>(workspace);
-  CUtensorMap tq, tg, tk, tv, tdq;
+  CUtensorMap tq, tg, tk, tv, tdq, tqn, tgn;
   mla_status st;
   if ((st = cross_tmap(&tq, a.q, d.B, d.n_q, d.H, D, d.q_row, kT)) != MLA_OK) return st;
   if ((st = cross_tmap(&tg, a.d_out, d.B, d.n_q, d.H, D, d.H * D, kT)) != MLA_OK) return st;
   if ((st = cross_tmap(&tk, a.k, d.B, d.n_kv, d.Hkv, D, d.k_row, kT)) != MLA_OK) return st;
   if ((st = cross_tmap(&tv, a.v, d.B, d.n_kv, d.Hkv, D, d.v_row, kT)) != MLA_OK) return st;
+  if ((st = cross_tmap(&tqn, a.q, d.B, d.n_q, d.H, D, d.q_row, kQN)) != MLA_OK) return st;
+  if ((st = cross_tmap(&tgn, a.d_out, d.B, d.n_q, d.H, D, d.H * D, kQN)) != MLA_OK) return st;
   if ((st = cross_tmap(&tdq, a.d_q, d.B, d.n_q, d.H, D, d.H * D, kT)) != MLA_OK) return st;
   CrossBwdParams p;
   p.B = d.B; p.H = d.H; p.Hkv = d.Hkv; p.rep = d.H / d.Hkv; p.n_q = d.n_q; p.n_kv = d.n_kv;
   p.n_pad = l.n_pad;
-  p.q_tiles = l.n_pad / kT;
+  p.q_tiles = l.q_tiles; p.qn_tiles = l.qn_tiles;
   p.items = p.q_tiles * d.H * d.B;      // fewer than 2^31: every item has at least one query row
   p.kv_tiles = l.kv_tiles; p.splits = l.splits;
   p.scale = d.scale; p.scale_log2 = d.scale * kLog2e;
@@ -849,7 +895,7 @@ mla_status bwd_impl(const CrossDims& d, const CrossBwdArgs& a, void* workspace, 
   MLA_CUDA_TRY(launch_pdl(cross_dq_tc_kernel<D>, dim3(std::min(p.items, 148)), dim3(kThreads),
                           DqShape<D>::kSmem, s, tq, tg, tk, tv, tdq, static_cast<bf16*>(a.d_q), p));
   MLA_CUDA_TRY(launch_pdl(cross_dkv_tc_kernel<D>, dim3(tiles * l.splits),
-                          dim3(kThreadsKV), DkvShape<D>::kSmem, s, tq, tg, tk, tv, p));
+                          dim3(kThreadsKV), DkvShape<D>::kSmem, s, tqn, tgn, tk, tv, p));
   MLA_CUDA_TRY(launch_pdl(cross_dkv_reduce_kernel<D>, dim3(tiles * (D / 8)),
                           dim3(kT), 0, s, static_cast<bf16*>(a.d_k), static_cast<bf16*>(a.d_v), p));
   return MLA_OK;
