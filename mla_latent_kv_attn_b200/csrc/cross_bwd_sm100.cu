@@ -1,5 +1,5 @@
 // cross_bwd_sm100.cu - the gradients of the cross attention on the sm_100a tensor cores, for bf16
-// with head widths 64 and 128 (the mathematics are in cross_simt.cu).  Four launches:
+// with head widths 64 and 128 (the mathematics are in cross_simt.cu).  Three or four launches:
 //
 //   stats   per query row lse log2(e) and delta = g . o, in arrays padded to whole 128-row tiles (a
 //           padding row's lse is +infinity, so that its probabilities are zero)
@@ -7,11 +7,15 @@
 //             S = Q K_j^T, dP = G V_j^T, dS = P o (dP - delta) scale, dQ += dS K_j
 //   dK, dV  a 128-row tile of states per block, streaming the query tiles of the heads that share
 //           it:  S^T = K Q_i^T, dP^T = V G_i^T, dV += P^T G_i, dK += dS^T Q_i
-//   reduce  the blocks' sums of one tile of states added in a fixed order and rounded once
+//   reduce  where several blocks share a tile's queries: their sums added in a fixed order and
+//           rounded once
 //
 // S and dP are computed twice (7 products where 5 would do): a single pass would have to add dQ
 // over blocks, in an order that changes from run to run or in fp32 copies that cost more memory
 // traffic than the two products (115 MB for 4680 queries, 12 heads and 512 states).
+// (The statistics inside the dQ kernel, by warps of their own, and the sum by the last block of each
+// tile made that call 75 us instead of 70: the first tiles wait for rows from DRAM, and 48 blocks do
+// the sum of all.)
 // P and dS are rounded to bf16 as operands (in TMEM); every product accumulates in fp32 in TMEM.
 // Every wait is bounded; one that runs out writes MLA_ERR_DEVICE_TIMEOUT
 // to dev_status.
@@ -137,33 +141,39 @@ __global__ void __launch_bounds__(256)
   constexpr int kPer = D / 16;
   const int h = blockIdx.y, b = blockIdx.z;
   const int64_t bh = static_cast<int64_t>(b) * H + h;
-  const int l16 = threadIdx.x % 16;
+  const int l16 = threadIdx.x % 16, i0 = blockIdx.x * kStatRows + threadIdx.x / 16;
+  constexpr int kRows = kStatRows / 16;
+  // every row's loads are on their way before the first is used
+  uint32_t x[kRows][kPer / 2], y[kRows][kPer / 2];
+  float l[kRows];
 #pragma unroll
-  for (int r0 = 0; r0 < kStatRows; r0 += 16) {
-    const int i = blockIdx.x * kStatRows + r0 + threadIdx.x / 16;
+  for (int k = 0; k < kRows; ++k) {
+    const int i = i0 + 16 * k;
+    const int64_t at = ((static_cast<int64_t>(b) * n_q + min(i, n_q - 1)) * H + h) * D + l16 * kPer;
+    if constexpr (D == 128) {
+      *reinterpret_cast<uint4*>(x[k]) = *reinterpret_cast<const uint4*>(out + at);
+      *reinterpret_cast<uint4*>(y[k]) = *reinterpret_cast<const uint4*>(g + at);
+    } else {
+      *reinterpret_cast<uint2*>(x[k]) = *reinterpret_cast<const uint2*>(out + at);
+      *reinterpret_cast<uint2*>(y[k]) = *reinterpret_cast<const uint2*>(g + at);
+    }
+    l[k] = i < n_q ? lse[bh * n_q + i] * kLog2e : INFINITY;
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int i = i0 + 16 * k;
     float s = 0.f;
-    if (i < n_q) {
-      const int64_t at = ((static_cast<int64_t>(b) * n_q + i) * H + h) * D + l16 * kPer;
-      uint32_t x[kPer / 2], y[kPer / 2];
-      if constexpr (D == 128) {
-        *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(out + at);
-        *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(g + at);
-      } else {
-        *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(out + at);
-        *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(g + at);
-      }
 #pragma unroll
-      for (int k = 0; k < kPer / 2; ++k) {
-        // a bf16 is the upper half of its float
-        s = fmaf(__uint_as_float(x[k] << 16), __uint_as_float(y[k] << 16), s);
-        s = fmaf(__uint_as_float(x[k] & 0xffff0000u), __uint_as_float(y[k] & 0xffff0000u), s);
-      }
+    for (int e = 0; e < kPer / 2; ++e) {
+      // a bf16 is the upper half of its float
+      s = fmaf(__uint_as_float(x[k][e] << 16), __uint_as_float(y[k][e] << 16), s);
+      s = fmaf(__uint_as_float(x[k][e] & 0xffff0000u), __uint_as_float(y[k][e] & 0xffff0000u), s);
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (l16 == 0 && i < n_pad) {
-      lse2[bh * n_pad + i] = i < n_q ? lse[bh * n_q + i] * kLog2e : INFINITY;
-      delta[bh * n_pad + i] = s;
+    if (l16 == 0) {
+      lse2[bh * n_pad + i] = l[k];
+      delta[bh * n_pad + i] = i < n_q ? s : 0.f;
     }
   }
 }
@@ -545,7 +555,8 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     cross_dkv_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_g,
                         const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, CrossBwdParams p) {
+                        const __grid_constant__ CUtensorMap tm_v, bf16* __restrict__ d_k,
+                        bf16* __restrict__ d_v, CrossBwdParams p) {
   using Sh = DkvShape<D>;
   constexpr int kTile = Sh::kTile, kQTile = Sh::kQTile, kStages = Sh::kStages;
   constexpr uint32_t kColDK = 0, kColDV = D;
@@ -604,8 +615,21 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
                     ? static_cast<int>(static_cast<int64_t>(work) * (split + 1) / p.splits) - first
                     : 0;
 
+  // row `row` of the tile's dK (0) or dV (1)
+  const auto grad_row = [&](int which, int row) {
+    return (which ? d_v : d_k) +
+           ((static_cast<int64_t>(b) * p.n_kv + tile * kT + row) * p.Hkv + kh) * D;
+  };
+
   if (n == 0) {
-    // (falls through to the end: nothing is written, the sum skips masked tiles)
+    // a tile of masked states: zeros, here or from the sum
+    if (p.splits == 1 && threadIdx.x < 2 * kT) {
+      const int row = threadIdx.x % kT;
+      if (tile * kT + row < p.n_kv) {
+        uint4* dst = reinterpret_cast<uint4*>(grad_row(threadIdx.x / kT, row));
+        for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
   } else if (warp == kProducerWarp) {
     if (lane == 0) {
       const uint32_t kb = smem_u32(&sh.k_full), vb = smem_u32(&sh.v_full);
@@ -759,19 +783,39 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     if (ok) ok = all(wait2(sh.dv_done, n - 1) && wait2(sh.dk_done, n - 1));
     if (ok) {
       tc_fence_after();
-      // four columns of 32 rows are 512 consecutive bytes
-      const int64_t tile_at =
-          (((static_cast<int64_t>(split) * p.B + b) * p.Hkv + kh) * p.kv_tiles + tile) * (kT * D);
-      const int64_t half = static_cast<int64_t>(p.splits) * p.B * p.Hkv * p.kv_tiles * (kT * D);
+      if (p.splits == 1) {
+        // the gradients themselves; rows of masked states are zero
+        const int j = tile * kT + row;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t r[32];
-        tmem_ld32_wait(tl + (grp == 0 ? kColDK : kColDV) + c, r);
-        float4* dst = reinterpret_cast<float4*>(p.partial + grp * half + tile_at) + (c / 4) * kT + row;
+        for (int c = 0; c < D; c += 32) {
+          uint32_t r[32];
+          tmem_ld32_wait(tl + (grp == 0 ? kColDK : kColDV) + c, r);
+          uint32_t v[16];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          dst[k * kT] = make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
-                                    __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
+          for (int e = 0; e < 16; ++e)
+            v[e] = j < len ? pack_bf16x2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])) : 0u;
+          if (j < p.n_kv) {
+            uint4* dst = reinterpret_cast<uint4*>(grad_row(grp, row) + c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          }
+        }
+      } else {
+        // four columns of 32 rows are 512 consecutive bytes
+        const int64_t tile_at =
+            (((static_cast<int64_t>(split) * p.B + b) * p.Hkv + kh) * p.kv_tiles + tile) * (kT * D);
+        const int64_t half = static_cast<int64_t>(p.splits) * p.B * p.Hkv * p.kv_tiles * (kT * D);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t r[32];
+          tmem_ld32_wait(tl + (grp == 0 ? kColDK : kColDV) + c, r);
+          float4* dst = reinterpret_cast<float4*>(p.partial + grp * half + tile_at) + (c / 4) * kT + row;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k * kT] = make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
+                                      __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
+        }
       }
     }
   }
@@ -854,7 +898,7 @@ BwdLayout bwd_layout(const CrossDims& d) {
   l.lse2 = 0;
   l.delta = stat;
   l.partial = 2 * stat;
-  l.bytes = l.partial + 2 * static_cast<size_t>(l.splits) * d.B * d.Hkv * l.kv_tiles * kT * d.d *
+  l.bytes = l.partial + 2 * static_cast<size_t>(l.splits == 1 ? 0 : l.splits) * d.B * d.Hkv * l.kv_tiles * kT * d.d *
                             sizeof(float);
   return l;
 }
@@ -895,7 +939,9 @@ mla_status bwd_impl(const CrossDims& d, const CrossBwdArgs& a, void* workspace, 
   MLA_CUDA_TRY(launch_pdl(cross_dq_tc_kernel<D>, dim3(std::min(p.items, 148)), dim3(kThreads),
                           DqShape<D>::kSmem, s, tq, tg, tk, tv, tdq, static_cast<bf16*>(a.d_q), p));
   MLA_CUDA_TRY(launch_pdl(cross_dkv_tc_kernel<D>, dim3(tiles * l.splits),
-                          dim3(kThreadsKV), DkvShape<D>::kSmem, s, tqn, tgn, tk, tv, p));
+                          dim3(kThreadsKV), DkvShape<D>::kSmem, s, tqn, tgn, tk, tv,
+                          static_cast<bf16*>(a.d_k), static_cast<bf16*>(a.d_v), p));
+  if (l.splits == 1) return MLA_OK;
   MLA_CUDA_TRY(launch_pdl(cross_dkv_reduce_kernel<D>, dim3(tiles * (D / 8)),
                           dim3(kT), 0, s, static_cast<bf16*>(a.d_k), static_cast<bf16*>(a.d_v), p));
   return MLA_OK;
