@@ -557,8 +557,8 @@ mla_status mla_attention_fwd_from_cq_q4(const mla_config* cfg, const void* c_q, 
  *   rows past kv_len are zero).  A sample with kv_len 0 has zero gradients, one with kv_len 1 zero
  *   d_q and d_k (its softmax is constant).
  * Workspace: mla_cross_attention_bwd_workspace_bytes (0 for a bad configuration), 256-byte
- * aligned.  Results do not depend on the order in which blocks run: the same call gives the same
- * bits.
+ * aligned; what it holds on entry does not matter, and calls that may run at the same time need one
+ * each.  Results do not depend on the order in which blocks run: the same call gives the same bits.
  *
  * dtype as in mla_config.  kernel_path: MLA_PATH_AUTO (tensor cores for bf16 with d_head 64 or
  * 128, CUDA cores otherwise) or MLA_PATH_SIMT (CUDA cores).  d_head <= 256.  Outputs must not

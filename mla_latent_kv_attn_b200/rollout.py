@@ -487,15 +487,16 @@ class EncoderStates:
     """One layer's keys and values of an encoder's states (a prompt), projected once and attended
     by every chunk and denoising step: k, v [B, n_kv, H_kv, d_head] and the number of valid states
     per sample, kv_len [B] (None: all).  attend() is the layer's cross attention, backward() its
-    gradients; the backward's workspace is allocated by the first backward call, so backward calls
-    of one object are ordered on one stream."""
+    gradients.  The backward's workspaces (one per size asked for) belong to the object and stay as
+    long as it does, for graphs that captured them; so the backward calls of one object are ordered
+    on one stream."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, n_heads: int,
                  kv_len: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None):
         self.k, self.v, self.kv_len = k, v, kv_len
         self.n_heads, self.softmax_scale = n_heads, softmax_scale
         self.dev_status = torch.zeros((1,), device=k.device, dtype=torch.int32)
-        self.workspace = None
+        self.workspaces = {}
 
     def config(self, n_q: int):
         B, n_kv, n_kv_heads, d_head = self.k.shape
@@ -514,8 +515,8 @@ class EncoderStates:
     def backward(self, q, out, lse, d_out, d_q, d_k, d_v, stream=None) -> None:
         cc = self.config(q.shape[1])
         need = api.mla_cross_attention_bwd_workspace_bytes(cc)
-        if self.workspace is None or self.workspace.numel() < need:
-            self.workspace = torch.empty((need,), device=q.device, dtype=torch.uint8)
+        if need not in self.workspaces:
+            self.workspaces[need] = torch.empty((need,), device=q.device, dtype=torch.uint8)
         api.mla_cross_attention_bwd(cc, q, self.k, self.v, out, lse, d_out, d_q, d_k, d_v,
-                                    self.workspace, kv_len=self.kv_len,
+                                    self.workspaces[need], kv_len=self.kv_len,
                                     dev_status=self.dev_status, stream=stream)

@@ -293,6 +293,61 @@ def test_encoder_states_serve_chunks_and_training():
     assert int(e.dev_status) == 0
 
 
+def test_layer_sized_call():
+    """A chunk of the Wan-shaped layer against prompts of two lengths: every element of the first and
+    the last head (whose keys no other head shares) against the definition."""
+    lens = [512, 389]
+    c = Case(2, 4680, 512, 12, 12, 128, lens=lens, seed=11)
+    c.fwd()
+    c.bwd()
+    for h in (0, 11):
+        part = object.__new__(Case)
+        one = lambda t: t[:, :, h:h + 1]
+        part.cc = api.make_cross_config(batch=2, n_heads=1, n_kv_heads=1, d_head=128, n_q=4680,
+                                        n_kv=512)
+        part.dt, part.lens, part.status = c.dt, lens, c.status
+        part.q, part.k, part.v, part.g, part.out = map(one, (c.q, c.k, c.v, c.g, c.out))
+        part.lse = c.lse[:, h:h + 1]
+        part.grads = [one(t) for t in c.grads]
+        part.check()
+
+
+def test_gradients_of_many_queries_per_state_tile():
+    """Several blocks share a tile's queries and their sums are added; one block writes its own."""
+    for B, n_q, n_kv, H, Hkv, d, lens in ((1, 900, 100, 4, 1, 64, [99]), (1, 1500, 300, 2, 2, 128, [130]),
+                                          (2, 81, 129, 2, 1, 128, [129, 0])):
+        c = Case(B, n_q, n_kv, H, Hkv, d, lens=lens, seed=12)
+        c.fwd()
+        c.bwd()
+        c.check()
+        first = [t.clone() for t in c.grads]
+        for _ in range(3):
+            c.bwd()
+        assert all(torch.equal(a, b) for a, b in zip(first, c.grads))
+
+
+def test_calls_on_two_streams_at_once():
+    """Forward and backward of two problems side by side, each with its own workspace."""
+    a, b = Case(2, 700, 300, 4, 2, 128, lens=[300, 41]), Case(3, 500, 200, 8, 8, 64, seed=5)
+    want = []
+    for c in (a, b):
+        c.fwd()
+        c.bwd()
+        want.append([t.clone() for t in (c.out, c.lse, *c.grads)])
+        for t in (c.out, c.lse, *c.grads):
+            t.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for c, s in zip((a, b), streams):
+            c.fwd(stream=s)
+            c.bwd(stream=s)
+    torch.cuda.synchronize()
+    for c, w in zip((a, b), want):
+        assert all(torch.equal(x, y) for x, y in zip(w, (c.out, c.lse, *c.grads)))
+        assert int(c.status) == 0
+
+
 def test_bad_pointers_are_refused():
     c = Case(1, 8, 16, 2, 2, 64)
     host = torch.zeros(c.q.shape, dtype=c.dt)

@@ -343,7 +343,38 @@ def test_layer_stack_and_graphs_over_4_bit_rings():
     assert torch.equal(three.read(), one.read())
 
 
-def test_streamer_prefill_and_side_stream():
+def test_host_streamer_serves_4_bit_rings():
+    """Two rollouts in turn through one streamer: outputs and rings of each as when run alone."""
+    cfg = SMALL
+    c = api.make_config(cfg)
+    w = rollout.upload_weights(c, inputs.layer_weights(cfg))
+    xs = [[torch.from_numpy(inputs.chunk_x(cfg, ch, layer=r)).to(torch.bfloat16)
+           for ch in range(cfg.n_chunks)] for r in range(2)]
+    buf = rollout.ChunkBuffers(c, q4=True)
+    refs, rings = [], [rollout.RingQ4(c) for _ in range(2)]
+    for r in range(2):
+        refs.append([])
+        for ch in range(cfg.n_chunks):
+            buf.x.copy_(xs[r][ch])
+            refs[r].append(rollout.run_chunk(c, w, rings[r], buf, ch).cpu().clone())
+    served = [rollout.RingQ4(c) for _ in range(2)]
+    st = rollout.HostStreamer(c, w, served[0])
+    outs = [[torch.empty_like(refs[0][0]).pin_memory() for _ in range(cfg.n_chunks)]
+            for _ in range(2)]
+    for ch in range(cfg.n_chunks):
+        for r in range(2):
+            st.submit(ch, xs[r][ch].pin_memory(), outs[r][ch], ring=served[r])
+    st.finish()
+    torch.cuda.synchronize()
+    st.check_device_status()
+    for r in range(2):
+        for ch in range(cfg.n_chunks):
+            assert torch.equal(outs[r][ch], refs[r][ch]), (r, ch)
+        assert torch.equal(served[r].codes, rings[r].codes), r
+        assert torch.equal(served[r].scales, rings[r].scales), r
+
+
+def test_prefill_on_a_side_stream():
     cfg = SMALL
     c = api.make_config(cfg)
     w = rollout.upload_weights(c, inputs.layer_weights(cfg))
