@@ -48,25 +48,25 @@ struct CrossBwdParams {
   int32_t* dev_status;
 };
 
-// p = 2^(s scale - l) of kN columns of a row whose l is the same (dQ, l_step 0) or that of the column
+// p = 2^(s scale - l) of kN columns of a row, in place; l is the row's (dQ, l_step 0) or the column's
 // (dK, dV: neg_l2 holds kN / 2 pairs).
 template <int kN>
-__device__ __forceinline__ void probabilities(const uint32_t (&s)[kN], uint64_t scale2,
-                                              const uint64_t* neg_l2, int l_step, float* p) {
+__device__ __forceinline__ void probabilities(uint32_t* s, uint64_t scale2, const uint64_t* neg_l2,
+                                              int l_step) {
 #pragma unroll
   for (int k = 0; k < kN / 2; ++k) {
     float x0, x1;
     f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), scale2,
                      neg_l2[k * l_step]),
               x0, x1);
-    p[2 * k] = fast_exp2(x0);
-    p[2 * k + 1] = fast_exp2(x1);
+    s[2 * k] = __float_as_uint(fast_exp2(x0));
+    s[2 * k + 1] = __float_as_uint(fast_exp2(x1));
   }
 }
 
 // dS = p (dP scale - delta scale) of kN columns, as bf16 pairs.
 template <int kN>
-__device__ __forceinline__ void score_gradients(const uint32_t (&dp)[kN], const float* p,
+__device__ __forceinline__ void score_gradients(const uint32_t (&dp)[kN], const uint32_t* p,
                                                 uint64_t scale2, const uint64_t* neg_d2, int d_step,
                                                 uint32_t (&w)[kN / 2]) {
 #pragma unroll
@@ -74,7 +74,7 @@ __device__ __forceinline__ void score_gradients(const uint32_t (&dp)[kN], const 
     float d0, d1;
     f2_unpack(f2_mul(f2_fma(f2_pack(__uint_as_float(dp[2 * k]), __uint_as_float(dp[2 * k + 1])),
                             scale2, neg_d2[k * d_step]),
-                     f2_pack(p[2 * k], p[2 * k + 1])),
+                     f2_pack(__uint_as_float(p[2 * k]), __uint_as_float(p[2 * k + 1]))),
               d0, d1);
     w[k] = pack_bf16x2(d0, d1);
   }
@@ -433,16 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const int valid = w.len - j * kT - 64 * ch;
-        float pr[64];
-        {
-          uint32_t s[32];
-          tmem_ld32_wait(ts, s);
-          probabilities<32>(s, sl2, &nl2, 0, pr);
-          tmem_ld32_wait(ts + 32, s);
-          tc_fence_before();
-          mbar_arrive(smem_u32(&sh.s_free));
-          probabilities<32>(s, sl2, &nl2, 0, pr + 32);
-        }
+        uint32_t pr[64];                 // S, then P
+        tmem_ld64_wait(ts, pr);
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sh.s_free));
+        probabilities<64>(pr, sl2, &nl2, 0);
         ok = wait_all(sh.dp_full[t & 1], t >> 1);
         if (!ok) break;
         tc_fence_after();
@@ -720,26 +715,24 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
       tc_fence_after();
       const float4* lse4 = reinterpret_cast<const float4*>(stats + s * (Sh::kStatBytes / 4));
       const float4* del4 = lse4 + kQN / 4;
-      float pr[kQN];
+      uint32_t pr[kQN];                // S^T, then P^T
       uint32_t w[2][kQH / 2];
+      tmem_ld80_wait(tl + kColS, pr);
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sh.s_free[i & 1]));
 #pragma unroll
       for (int c = 0; c < kQN; c += kQH) {
-        uint32_t raw[kQH];
         uint64_t nl2[kQH / 2];
-        tmem_ld40_wait(tl + kColS + c, raw);
-        if (c + kQH == kQN) {
-          tc_fence_before();
-          mbar_arrive(smem_u32(&sh.s_free[i & 1]));
-        }
 #pragma unroll
         for (int k = 0; k < kQH / 4; ++k) {
           const float4 l = lse4[c / 4 + k];
           nl2[2 * k] = f2_mul(f2_pack(l.x, l.y), neg2);
           nl2[2 * k + 1] = f2_mul(f2_pack(l.z, l.w), neg2);
         }
-        probabilities<kQH>(raw, sl2, nl2, 1, pr + c);
+        probabilities<kQH>(pr + c, sl2, nl2, 1);
 #pragma unroll
-        for (int k = 0; k < kQH / 2; ++k) w[c / kQH][k] = pack_bf16x2(pr[c + 2 * k], pr[c + 2 * k + 1]);
+        for (int k = 0; k < kQH / 2; ++k)
+          w[c / kQH][k] = pack_bf16x2(__uint_as_float(pr[c + 2 * k]), __uint_as_float(pr[c + 2 * k + 1]));
       }
       // dV(i-1) has read P^T(i-1)
       if (i > 0) ok = all(wait2(sh.dv_done, i - 1));
