@@ -14,8 +14,8 @@ import torch
 
 from . import _lib
 from ._lib import (MLA_APPEND, MLA_BF16, MLA_FP32, MLA_PATH_AUTO, MLA_PATH_SIMT,
-                   MLA_PATH_TC_PAIR, MLA_PATH_TC_SINGLE, MLA_PROJECT, MLA_PROJECT_AND_APPEND, MLAConfigC, MLACrossConfigC,
-                   MLAError)
+                   MLA_PATH_TC_PAIR, MLA_PATH_TC_SINGLE, MLA_PROJECT, MLA_PROJECT_AND_APPEND, MLAConfigC,
+                   MLACrossConfigC, MLAError)
 
 __all__ = [
     "make_config", "torch_dtype", "mla_config_check", "mla_cache_append", "mla_rope3d",
@@ -61,9 +61,9 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None) -> Option
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if shape is not None and t.shape != shape:
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t.data_ptr()      # (a list as shape)
+    return t.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:

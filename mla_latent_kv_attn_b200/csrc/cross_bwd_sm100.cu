@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n;
     }
   }
+  settle_after_abort(abort_flag);
   tc_fence_before();
   __syncthreads();
   if (warp == kIssuerA) {
@@ -812,6 +813,7 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
       }
     }
   }
+  settle_after_abort(abort_flag);
   tc_fence_before();
   __syncthreads();
   if (warp == kIssuerA) {
@@ -891,8 +893,9 @@ BwdLayout bwd_layout(const CrossDims& d) {
   l.lse2 = 0;
   l.delta = stat;
   l.partial = 2 * stat;
-  l.bytes = l.partial + 2 * static_cast<size_t>(l.splits == 1 ? 0 : l.splits) * d.B * d.Hkv * l.kv_tiles * kT * d.d *
-                            sizeof(float);
+  const int sums = l.splits == 1 ? 0 : l.splits;
+  l.bytes = l.partial +
+            2 * static_cast<size_t>(sums) * d.B * d.Hkv * l.kv_tiles * kT * d.d * sizeof(float);
   return l;
 }
 

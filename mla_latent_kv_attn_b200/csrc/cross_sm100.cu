@@ -528,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n_item;
     }
   }
+  settle_after_abort(abort_flag);
   tc_fence_before();
   __syncthreads();
   if (warp == kIssuerWarp) {

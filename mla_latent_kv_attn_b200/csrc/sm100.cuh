@@ -83,6 +83,15 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity
   }
 }
 
+// Behind the last role of a CTA: after a wait that ran out, some 1 ms in which copies and products
+// still in flight end, so that they find the CTA's shared memory and TMEM there.
+__device__ __forceinline__ void settle_after_abort(const volatile int* abort_flag) {
+  if (*abort_flag == 0) return;
+  const long long start = clock64();
+  while (clock64() - start < (1 << 21)) {
+  }
+}
+
 // ---- TMA (tiled bulk tensor loads into this CTA's shared memory, no multicast) -------------
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
