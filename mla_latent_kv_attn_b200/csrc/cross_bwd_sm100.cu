@@ -16,9 +16,11 @@
 // (The statistics inside the dQ kernel, by warps of their own, and the sum by the last block of each
 // tile made that call 75 us instead of 70: the first tiles wait for rows from DRAM, and 48 blocks do
 // the sum of all.)
+// Measured: 4680 queries, 512 states, 12 heads of 128: 70.7 us a call, 521 TFLOP/s over the five products
+// of the formula and 729 over the seven computed (0.44 of the measured peak), of which about 8 us are
+// the statistics, 26 dQ, 32 dK and dV and 7 the sum; batch 4 with drawn lengths: 249 us.
 // P and dS are rounded to bf16 as operands (in TMEM); every product accumulates in fp32 in TMEM.
-// Every wait is bounded; one that runs out writes MLA_ERR_DEVICE_TIMEOUT
-// to dev_status.
+// Every wait is bounded; one that runs out writes MLA_ERR_DEVICE_TIMEOUT to dev_status.
 #include "cross_tc.cuh"
 
 namespace mla {

@@ -24,6 +24,10 @@
 // and the CUDA cores in turn (6000 cycles a pair of tiles, against 2048 of products and 4500 as it is).
 // States past a sample's length are masked: their scores become -infinity by selection, and their
 // value rows are overwritten with zeros in shared memory (0 * NaN would reach O).
+// Measured: 4680 queries, 512 states, 12 heads of 128: 24.8 us a call, 594 TFLOP/s (0.36 of the measured
+// peak; 2.5 rounds of items, and the products' hand-overs bound each); batch 2, 1333 queries, up to
+// 1501 states, 16 heads of 64 on 4: 42 us, bound by the exponentials (35.5 without them); one query:
+// 9.3 us, the host's side of the call.
 #include "cross_tc.cuh"
 
 namespace mla {

@@ -19,6 +19,9 @@
 // minus a bias are the scale byte.  All three passes are bound by memory, or by latency where they
 // move a few megabytes: a thread per group or half group, no shared memory, and few
 // instructions a value (no division, no conversion between integers and floats).
+// Measured (Wan widths): appending 37,440 tokens and reading 112,320 back 24 us for both, 13 us of
+// bytes; 4680 and 9360 tokens 12.6 us, the host's side of two calls; the pass before the attention over
+// 21 frames of 252 tokens in two samples 7.6 us cold.
 #include <cuda_fp16.h>
 
 #include "kernels.h"
