@@ -252,7 +252,8 @@ __device__ __forceinline__ void rope_key_row(const T* __restrict__ cache,
 // completed and its memory writes are visible.  Every CTA calls grid_dep_wait() before its first
 // access to global memory and unconditionally (so a kernel never completes before the one it
 // follows), then grid_dep_launch() to let the next kernel be scheduled.  Both are no-ops in a
-// kernel launched without the attribute.
+// kernel launched without the attribute.  (Two kernels of cross_bwd_sm100.cu call grid_dep_wait()
+// later, behind work that needs nothing of the kernel before them.)
 __device__ __forceinline__ void grid_dep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

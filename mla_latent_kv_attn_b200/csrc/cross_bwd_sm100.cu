@@ -1,24 +1,27 @@
 // cross_bwd_sm100.cu - the gradients of the cross attention on the sm_100a tensor cores, for bf16
-// with head widths 64 and 128 (the mathematics are in cross_simt.cu).  Three or four launches:
+// with head widths 64 and 128 (the mathematics are in cross_simt.cu).  Three launches:
 //
 //   stats   per query row lse log2(e) and delta = g . o, in arrays padded to whole 128-row tiles (a
 //           padding row's lse is +infinity, so that its probabilities are zero)
-//   dQ      a 128-row query tile per item, streaming the states' tiles:
-//             S = Q K_j^T, dP = G V_j^T, dS = P o (dP - delta) scale, dQ += dS K_j
 //   dK, dV  a 128-row tile of states per block, streaming the query tiles of the heads that share
 //           it:  S^T = K Q_i^T, dP^T = V G_i^T, dV += P^T G_i, dK += dS^T Q_i
-//   reduce  where several blocks share a tile's queries: their sums added in a fixed order and
-//           rounded once
+//   dQ      a 128-row query tile per item, streaming the states' tiles:
+//             S = Q K_j^T, dP = G V_j^T, dS = P o (dP - delta) scale, dQ += dS K_j
+//           and, where several blocks share a tile of states, the sums of their dK and dV, added in a
+//           fixed order and rounded once
 //
+// The launches overlap: each grid starts while the one before it ends and waits for it where it needs
+// its results (stats -> dK, dV: the statistics; dK, dV -> dQ: only the sums) and once more at its end,
+// so that the end of the last says that all have ended.  One after the other, and with the sums in a
+// launch of their own, the call took 69 us instead of 63.
 // S and dP are computed twice (7 products where 5 would do): a single pass would have to add dQ
 // over blocks, in an order that changes from run to run or in fp32 copies that cost more memory
 // traffic than the two products (115 MB for 4680 queries, 12 heads and 512 states).
-// (The statistics inside the dQ kernel, by warps of their own, and the sum by the last block of each
-// tile made that call 75 us instead of 70: the first tiles wait for rows from DRAM, and 48 blocks do
-// the sum of all.)
-// Measured: 4680 queries, 512 states, 12 heads of 128: 70.7 us a call, 521 TFLOP/s over the five products
-// of the formula and 729 over the seven computed (0.44 of the measured peak), of which about 8 us are
-// the statistics, 26 dQ, 32 dK and dV and 7 the sum; batch 4 with drawn lengths: 249 us.
+// (The statistics inside the dQ kernel, by warps of their own, made that call 75 us instead of 70: the
+// first tiles wait for rows from DRAM.)
+// Measured: 4680 queries, 512 states, 12 heads of 128: 63 us a call, 585 TFLOP/s over the five products
+// of the formula and 819 over the seven computed (0.50 of the measured peak); batch 4 with mixed
+// lengths 180 us; batch 2, 1333 queries, up to 333 states, 16 heads of 64 on 4: 35 us.
 // P and dS are rounded to bf16 as operands (in TMEM); every product accumulates in fp32 in TMEM.
 // Every wait is bounded; one that runs out writes MLA_ERR_DEVICE_TIMEOUT to dev_status.
 #include "cross_tc.cuh"
@@ -33,7 +36,7 @@ constexpr int kT = kCrossTile;            // rows of every tile
 constexpr int kSoftmaxThreads = 256;      // two threads per row, each with half of the columns
 constexpr int kProducerWarp = 8;
 constexpr int kIssuerA = 9, kIssuerB = 10;
-constexpr int kStoreWarp = 11;
+constexpr int kSumWarp = 11;
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 
@@ -47,6 +50,7 @@ struct CrossBwdParams {
   const float* lse2;                      // [B, H, n_pad]
   const float* delta;                     // [B, H, n_pad]
   float* partial;                         // [2, splits, B, Hkv, kv_tiles, D/4, 128, 4]
+  int* next_item;                         // dQ: the next item that no block has
   int32_t* dev_status;
 };
 
@@ -137,9 +141,11 @@ template <int D>
 __global__ void __launch_bounds__(256)
     cross_stats_kernel(const bf16* __restrict__ out, const bf16* __restrict__ g,
                        const float* __restrict__ lse, float* __restrict__ lse2,
-                       float* __restrict__ delta, int H, int n_q, int n_pad) {
+                       float* __restrict__ delta, int* next_item, int first_item, int H, int n_q,
+                       int n_pad) {
   grid_dep_wait();
   grid_dep_launch();
+  if ((threadIdx.x | blockIdx.x | blockIdx.y | blockIdx.z) == 0) *next_item = first_item;
   constexpr int kPer = D / 16;
   const int h = blockIdx.y, b = blockIdx.z;
   const int64_t bh = static_cast<int64_t>(b) * H + h;
@@ -182,6 +188,45 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------------------------------- dQ
 
+// dK and dV where several blocks share a tile of states: the sums over them, in order.  A warp takes
+// 32 columns of 32 rows, a row per thread; rows of masked states are 0.  The block's next piece is
+// number `*next`; false when there is none.
+template <int D>
+__device__ __forceinline__ bool sum_piece(const CrossBwdParams& p, bf16* d_k, bf16* d_v, int* next,
+                                          int lane) {
+  constexpr int kRowParts = kT / 32, kColParts = D / 32;
+  int e = lane == 0 ? atomicAdd(next, 1) : 0;
+  e = blockIdx.x + gridDim.x * __shfl_sync(0xffffffffu, e, 0);
+  const int bt = e / (2 * kRowParts * kColParts);
+  if (bt >= p.B * p.Hkv * p.kv_tiles) return false;
+  const int row = e % kRowParts * 32 + lane, c = e / kRowParts % kColParts * 32;
+  const int which = e / (kRowParts * kColParts) % 2;
+  const int tile = bt % p.kv_tiles, kh = bt / p.kv_tiles % p.Hkv, b = bt / p.kv_tiles / p.Hkv;
+  const int j = tile * kT + row;
+  if (j >= p.n_kv) return true;
+  float4 a[8] = {};
+  if (j < cross_len(p.kv_len, b, p.n_kv)) {
+    const int64_t step = static_cast<int64_t>(p.B) * p.Hkv * p.kv_tiles * (kT * D);
+    const float4* src = reinterpret_cast<const float4*>(
+        p.partial + which * p.splits * step + static_cast<int64_t>(bt) * (kT * D)) + c / 4 * kT + row;
+#pragma unroll 2
+    for (int s = 0; s < p.splits; ++s, src += step / 4) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 v = __ldcg(src + k * kT);
+        a[k].x += v.x; a[k].y += v.y; a[k].z += v.z; a[k].w += v.w;
+      }
+    }
+  }
+  uint4* dst = reinterpret_cast<uint4*>(
+      (which ? d_v : d_k) + ((static_cast<int64_t>(b) * p.n_kv + j) * p.Hkv + kh) * D + c);
+#pragma unroll
+  for (int k = 0; k < 8; k += 2)
+    dst[k / 2] = make_uint4(pack_bf16x2(a[k].x, a[k].y), pack_bf16x2(a[k].z, a[k].w),
+                            pack_bf16x2(a[k + 1].x, a[k + 1].y), pack_bf16x2(a[k + 1].z, a[k + 1].w));
+  return true;
+}
+
 template <int D_>
 struct DqShape {
   static constexpr int D = D_;
@@ -195,8 +240,15 @@ struct DqShape {
 };
 constexpr uint32_t kDqColS = 0, kDqColDP = 128, kDqColAcc = 384;    // dP twice
 
+struct DqItem {
+  int b, h, q0, len;
+  __device__ __forceinline__ int tiles() const { return ceil_div(len, kT); }
+};
+constexpr int kItems = 4;                 // ring of items
+
 template <int kKStages, int kVStages>
 struct DqShared {
+  uint64_t item_full[kItems], item_empty[kItems];
   uint64_t q_full, q_empty;               // the item's Q, read by its last S
   uint64_t g_full, g_empty;               // the item's G, read by its last dP
   uint64_t k_full[kKStages], k_empty[kKStages];
@@ -208,29 +260,32 @@ struct DqShared {
   uint64_t staged, stage_free;            // and in shared memory; stored from there
   uint32_t tmem_base;
   int abort_flag;
+  int next_sum;                           // pieces of the sums that warps have taken
+  DqItem item[kItems];                    // q0 < 0: there are no more
 };
 
-struct DqItem {
-  int b, h, q0, len, nt;
-};
-
-// Item `it` (the last one when there is none).  Every role decodes an item ahead of its work, and
-// the softmax also reads its rows' statistics then: global memory is some 700 cycles away.
+// Item `it`; its length comes from global memory, some 700 cycles away.
 __device__ __forceinline__ DqItem dq_item(const CrossBwdParams& p, int it) {
-  it = min(it, p.items - 1);
-  DqItem w;
+  DqItem w{0, 0, -1, 0};
+  if (it >= p.items) return w;
   w.q0 = (it % p.q_tiles) * kT;
   const int bh = it / p.q_tiles;
   w.h = bh % p.H;
   w.b = bh / p.H;
   w.len = cross_len(p.kv_len, w.b, p.n_kv);
-  w.nt = ceil_div(w.len, kT);
   return w;
 }
 
 // Roles (384 threads): warps 0-7 softmax (warps w and w + 4 share 32 rows, each half of the
-// columns), 8 TMA producer, 9 issuer of S, 10 issuer of dP and dQ, 11 TMA stores of dQ.  The two dP
-// buffers let dP(j+1) run under the softmax of j, and S(j+1) runs once S(j) has been read.
+// columns), 8 TMA producer, 9 issuer of S, 10 issuer of dP and dQ, 11 sums of dK and dV, which
+// the softmax warps end after their items.  The two dP buffers let dP(j+1) run under the softmax of j, and S(j+1) runs once S(j) has been read.
+// The producer draws the block's items after its first from a counter that the statistics reset, an
+// item ahead of its loads, and hands them to the other roles; these take an item ahead of their work
+// (the softmax reads its rows' statistics then).  Blocks start as the dK, dV kernel's end and lengths
+// differ: with a fixed share for each block, the call of four samples took 216 us.
+// (Three more warps for the sums would leave each thread 128 registers, too few for the softmax.)
+// This grid starts block by block as the dK, dV kernel's blocks end: only the sums need its results.
+// (It starts when every block of that kernel runs and has seen the end of the statistics.)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -238,9 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CUtensorMap tm_dq, bf16* __restrict__ d_q,
-                       CrossBwdParams p) {
+                       bf16* __restrict__ d_k, bf16* __restrict__ d_v, CrossBwdParams p) {
   using Sh = DqShape<D>;
   constexpr int kTile = Sh::kTile, kKStages = Sh::kKStages, kVStages = Sh::kVStages;
+  static_assert(sizeof(DqShared<kKStages, kVStages>) <= 1024, "shared memory");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sQ = smem_u32(smem_raw), sG = sQ + kTile, sOut = sG + kTile, sK = sOut + kTile;
   const uint32_t sV = sK + kKStages * kTile;
@@ -250,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
+    sh.next_sum = 0;
     mbar_init(smem_u32(&sh.q_full), 1);
     mbar_init(smem_u32(&sh.q_empty), 1);
     mbar_init(smem_u32(&sh.g_full), 1);
@@ -258,6 +315,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sh.dp_full[b]), 1);
       mbar_init(smem_u32(&sh.dq_done[b]), 1);
+    }
+    for (int s = 0; s < kItems; ++s) {
+      mbar_init(smem_u32(&sh.item_full[s]), 1);
+      mbar_init(smem_u32(&sh.item_empty[s]), 2 + kSoftmaxThreads / 32);   // issuers, softmax warps
     }
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(smem_u32(&sh.k_full[s]), 1);
@@ -282,28 +343,58 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
-  grid_dep_wait();
   grid_dep_launch();
 
   const auto wait = [&](uint64_t& bar, uint32_t phase) {
     return mbar_wait_or_abort(smem_u32(&bar), phase & 1, abort_flag, p.dev_status);
   };
-  DqItem next = dq_item(p, blockIdx.x);
+  DqItem next = dq_item(p, blockIdx.x);       // every role finds the first item itself
+  // The next item, for a thread that others do not follow.
+  uint32_t n_items = 0;
+  const auto take = [&]() {
+    const int slot = n_items % kItems;
+    DqItem w{0, 0, -1, 0};
+    if (wait(sh.item_full[slot], n_items / kItems)) {
+      w = sh.item[slot];
+      mbar_arrive(smem_u32(&sh.item_empty[slot]));
+    }
+    ++n_items;
+    return w;
+  };
+  // The same for a warp.
+  const auto take_warp = [&]() {
+    const int slot = n_items % kItems;
+    DqItem w{0, 0, -1, 0};
+    if (__all_sync(0xffffffffu, wait(sh.item_full[slot], n_items / kItems))) w = sh.item[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.item_empty[slot]));
+    ++n_items;
+    return w;
+  };
 
   if (warp == kProducerWarp) {
     if (lane == 0) {
-      uint32_t n = 0, t = 0;              // items, tiles
+      uint32_t n = 0, t = 0;              // items with loads, tiles
       bool ok = true;
-      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+      const auto publish = [&](const DqItem& w) {
+        const int slot = n_items % kItems;
+        if (!wait(sh.item_empty[slot], n_items / kItems + 1)) return false;
+        sh.item[slot] = w;
+        mbar_arrive(smem_u32(&sh.item_full[slot]));
+        ++n_items;
+        return true;
+      };
+      while (ok && next.q0 >= 0) {
         const DqItem w = next;
-        next = dq_item(p, it + gridDim.x);
-        if (w.nt == 0) continue;
-        ok = wait(sh.q_empty, n + 1);
-        if (!ok) break;
-        const uint32_t qb = smem_u32(&sh.q_full), gb = smem_u32(&sh.g_full);
-        mbar_arrive_expect_tx(qb, kTile);
-        load_tile<D>(sQ, &tm_q, qb, w.h, w.q0, w.b);
-        for (int j = 0; j < w.nt && ok; ++j, ++t) {
+        const int id = atomicAdd(p.next_item, 1), nt = w.tiles();
+        if (nt > 0) {
+          ok = wait(sh.q_empty, n + 1);
+          if (!ok) break;
+          const uint32_t qb = smem_u32(&sh.q_full);
+          mbar_arrive_expect_tx(qb, kTile);
+          load_tile<D>(sQ, &tm_q, qb, w.h, w.q0, w.b);
+        }
+        for (int j = 0; j < nt && ok; ++j, ++t) {
           const int ks = t % kKStages, vs = t % kVStages;
           ok = wait(sh.k_empty[ks], t / kKStages + 1);
           if (!ok) break;
@@ -313,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j == 0) {
             ok = wait(sh.g_empty, n + 1);
             if (!ok) break;
+            const uint32_t gb = smem_u32(&sh.g_full);
             mbar_arrive_expect_tx(gb, kTile);
             load_tile<D>(sG, &tm_g, gb, w.h, w.q0, w.b);
           }
@@ -321,26 +413,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t vb = smem_u32(&sh.v_full[vs]);
           mbar_arrive_expect_tx(vb, kTile);
           load_tile<D>(sV + vs * kTile, &tm_v, vb, w.h / p.rep, j * kT, w.b);
+          if (j == 0) {
+            next = dq_item(p, id);
+            ok = publish(next);
+          }
         }
-        ++n;
+        if (nt == 0) {
+          next = dq_item(p, id);
+          ok = publish(next);
+        } else {
+          ++n;
+        }
       }
     }
   } else if (warp == kIssuerA) {
     if (lane == 0) {
       uint32_t n = 0, t = 0;
       bool ok = true;
-      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+      while (ok && next.q0 >= 0) {
         const DqItem w = next;
-        next = dq_item(p, it + gridDim.x);
-        if (w.nt == 0) continue;
+        next = take();
+        const int nt = w.tiles();
+        if (nt == 0) continue;
         ok = wait(sh.q_full, n);
-        for (int j = 0; j < w.nt && ok; ++j, ++t) {
+        for (int j = 0; j < nt && ok; ++j, ++t) {
           ok = wait(sh.k_full[t % kKStages], t / kKStages) && (t == 0 || wait(sh.s_free, t - 1));
           if (!ok) break;
           tc_fence_after();
           mma_tiles<D>(tmem + kDqColS, sQ, sK + (t % kKStages) * kTile);
           mma_commit(smem_u32(&sh.s_full));
-          if (j == w.nt - 1) mma_commit(smem_u32(&sh.q_empty));
+          if (j == nt - 1) mma_commit(smem_u32(&sh.q_empty));
         }
         ++n;
       }
@@ -361,13 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last) mma_commit(smem_u32(&sh.g_empty));
         return true;
       };
-      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+      while (ok && next.q0 >= 0) {
         const DqItem w = next;
-        next = dq_item(p, it + gridDim.x);
-        if (w.nt == 0) continue;
-        ok = wait(sh.g_full, n) && issue_dp(t, w.nt == 1);
-        for (int j = 0; j < w.nt && ok; ++j, ++t) {
-          if (j + 1 < w.nt) ok = issue_dp(t + 1, j + 2 == w.nt);
+        next = take();
+        const int nt = w.tiles();
+        if (nt == 0) continue;
+        ok = wait(sh.g_full, n) && issue_dp(t, nt == 1);
+        for (int j = 0; j < nt && ok; ++j, ++t) {
+          if (j + 1 < nt) ok = issue_dp(t + 1, j + 2 == nt);
           ok = ok && wait(sh.ds_full, t) && (j > 0 || n == 0 || wait(sh.acc_free, n - 1));
           if (!ok) break;
           tc_fence_after();
@@ -379,24 +482,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n;
       }
     }
-  } else if (warp == kStoreWarp) {
-    if (lane == 0) {
-      uint32_t n = 0;
-      bool ok = true;
-      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-        const DqItem w = next;
-        next = dq_item(p, it + gridDim.x);
-        if (w.nt == 0) continue;
-        ok = wait(sh.staged, n);
-        if (!ok) break;
-        for (int k = 0; k < D / 64; ++k)           // (rows past n_q are not written)
-          tma_store_4d(&tm_dq, sOut + k * kT * 128, 64 * k, w.h, w.q0, w.b);
-        bulk_commit_group();
-        bulk_wait_group_read<0>();
-        mbar_arrive(smem_u32(&sh.stage_free));
-        ++n;
+  } else if (warp == kSumWarp) {
+    if (p.splits > 1) {
+      grid_dep_wait();
+      while (sum_piece<D>(p, d_k, d_v, &sh.next_sum, lane)) {
       }
-      bulk_wait_group_all();
     }
   } else {
     const int ch = warp / 4, row = (warp % 4) * 32 + lane;
@@ -408,17 +498,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint32_t n = 0, t = 0;
     bool ok = true;
-    const auto stat_at = [&](const DqItem& w) {
-      return (static_cast<int64_t>(w.b) * p.H + w.h) * p.n_pad + w.q0 + row;
+    float next_l = 0.f, next_d = 0.f;
+    const auto read_stats = [&]() {
+      if (next.q0 < 0) return;
+      const int64_t at = (static_cast<int64_t>(next.b) * p.H + next.h) * p.n_pad + next.q0 + row;
+      next_l = p.lse2[at];
+      next_d = p.delta[at];
     };
-    float next_l = p.lse2[stat_at(next)], next_d = p.delta[stat_at(next)];
-    for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+    read_stats();
+    while (ok && next.q0 >= 0) {
       const DqItem w = next;
       const float nl = -next_l, row_delta = next_d;
-      next = dq_item(p, it + gridDim.x);
-      next_l = p.lse2[stat_at(next)];
-      next_d = p.delta[stat_at(next)];
-      if (w.nt == 0) {
+      next = take_warp();
+      read_stats();
+      const int nt = w.tiles();
+      if (nt == 0) {
         const int i = w.q0 + row;
         if (i < p.n_q) {
           uint4* o4 = reinterpret_cast<uint4*>(
@@ -430,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a single state's softmax is constant: its dS is zero
       const float sc = w.len == 1 ? 0.f : p.scale, nd = -row_delta * sc;
       const uint64_t nl2 = f2_pack(nl, nl), sc2 = f2_pack(sc, sc), nd2 = f2_pack(nd, nd);
-      for (int j = 0; j < w.nt; ++j, ++t) {
+      for (int j = 0; j < nt; ++j, ++t) {
         ok = wait_all(sh.s_full, t);
         if (!ok) break;
         tc_fence_after();
@@ -470,6 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(smem_u32(&sh.ds_full));
       }
       if (!ok) break;
+      if (threadIdx.x == 0 && n > 0) {       // its copy out of shared memory, an item ago
+        bulk_wait_group_read<0>();
+        mbar_arrive(smem_u32(&sh.stage_free));
+      }
       ok = wait_all(sh.dq_done[(t - 1) & 1], (t - 1) >> 1) &&
            (n == 0 || wait_all(sh.stage_free, n - 1));
       if (!ok) break;
@@ -492,7 +590,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(smem_u32(&sh.acc_free));
       fence_proxy_async_smem();
       mbar_arrive(smem_u32(&sh.staged));
+      if (threadIdx.x == 0 && wait(sh.staged, n)) {
+        for (int k = 0; k < D / 64; ++k)           // (rows past n_q are not written)
+          tma_store_4d(&tm_dq, sOut + k * kT * 128, 64 * k, w.h, w.q0, w.b);
+        bulk_commit_group();
+      }
+      __syncwarp();
       ++n;
+    }
+    if (threadIdx.x == 0) bulk_wait_group_all();
+    __syncwarp();
+    if (ok && p.splits > 1) {
+      grid_dep_wait();
+      while (sum_piece<D>(p, d_k, d_v, &sh.next_sum, lane)) {
+      }
     }
   }
   settle_after_abort(abort_flag);
@@ -502,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  grid_dep_wait();      // the end of this grid says that those before it have ended
 }
 
 // ------------------------------------------------------------------------------------- dK, dV
@@ -598,8 +710,6 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
-  grid_dep_wait();
-  grid_dep_launch();
 
   const auto wait = [&](uint64_t& bar, uint32_t phase) {
     return mbar_wait_or_abort(smem_u32(&bar), phase & 1, abort_flag, p.dev_status);
@@ -644,8 +754,6 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
         const int64_t so = (static_cast<int64_t>(b) * p.H + h) * p.n_pad + q0;
         mbar_arrive_expect_tx(qb, kQTile + Sh::kStatBytes);
         load_tile<D, kQN>(sQ + s * kQTile, &tm_q, qb, h, q0, b);
-        bulk_load(st, p.lse2 + so, kQN * 4, qb);
-        bulk_load(st + kQN * 4, p.delta + so, kQN * 4, qb);
         if (i == 0) {
           mbar_arrive_expect_tx(vb, kTile);
           load_tile<D>(sV, &tm_v, vb, kh, tile * kT, b);
@@ -655,6 +763,12 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
         const uint32_t gb = smem_u32(&sh.g_full[s]);
         mbar_arrive_expect_tx(gb, kQTile);
         load_tile<D, kQN>(sG + s * kQTile, &tm_g, gb, h, q0, b);
+        if (i == 0) {
+          grid_dep_wait();          // the statistics
+          grid_dep_launch();
+        }
+        bulk_load(st, p.lse2 + so, kQN * 4, qb);
+        bulk_load(st + kQN * 4, p.delta + so, kQN * 4, qb);
       }
     }
   } else if (warp == kIssuerA) {
@@ -822,50 +936,18 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  grid_dep_wait();      // (a block without work)
 }
 
-// Sum over the splits, in order, of 16 columns of one row: a thread.  Rows of masked states are 0.
-template <int D>
-__global__ void __launch_bounds__(kT)
-    cross_dkv_reduce_kernel(bf16* __restrict__ d_k, bf16* __restrict__ d_v, CrossBwdParams p) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int c16 = blockIdx.x % (D / 16), which = blockIdx.x / (D / 16) % 2;
-  const int bt = blockIdx.x / (D / 8);
-  const int tile = bt % p.kv_tiles, kh = bt / p.kv_tiles % p.Hkv, b = bt / p.kv_tiles / p.Hkv;
-  const int j = tile * kT + threadIdx.x;
-  if (j >= p.n_kv) return;
-  const int len = cross_len(p.kv_len, b, p.n_kv);
-  float4 a[4] = {};
-  if (j < len) {
-    const int64_t half = static_cast<int64_t>(p.B) * p.Hkv * p.kv_tiles * (kT * D);
-    const float4* src = reinterpret_cast<const float4*>(
-        p.partial + which * p.splits * half +
-        ((static_cast<int64_t>(b) * p.Hkv + kh) * p.kv_tiles + tile) * (kT * D)) +
-        4 * c16 * kT + threadIdx.x;
-    for (int s = 0; s < p.splits; ++s, src += half / 4) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 v = src[k * kT];
-        a[k].x += v.x; a[k].y += v.y; a[k].z += v.z; a[k].w += v.w;
-      }
-    }
-  }
-  uint4 o[2];
-  o[0] = make_uint4(pack_bf16x2(a[0].x, a[0].y), pack_bf16x2(a[0].z, a[0].w),
-                    pack_bf16x2(a[1].x, a[1].y), pack_bf16x2(a[1].z, a[1].w));
-  o[1] = make_uint4(pack_bf16x2(a[2].x, a[2].y), pack_bf16x2(a[2].z, a[2].w),
-                    pack_bf16x2(a[3].x, a[3].y), pack_bf16x2(a[3].z, a[3].w));
-  uint4* dst = reinterpret_cast<uint4*>(
-      (which ? d_v : d_k) + ((static_cast<int64_t>(b) * p.n_kv + j) * p.Hkv + kh) * D + 16 * c16);
-  dst[0] = o[0];
-  dst[1] = o[1];
-}
-
-// Blocks per tile of states: of the counts that give every block at least one query tile, the one
-// whose waves of 148 blocks take the fewest steps (a block costs about three steps beside its query
-// tiles), the smallest on a tie: each more adds sums to write and read.
+// Blocks per tile of states.  With a tile for every SM none is shared: dQ fills the SMs that the last
+// tiles leave (4 samples of 4680 queries, 12 heads, 512 states: 178 us against 192 with three blocks
+// per tile at mixed lengths, 247 against 233 at full ones; 2 samples of 2000 queries, 40 heads: 169
+// against 195).  Otherwise, of the counts that give every block at least one query tile, the one whose
+// waves of 148 blocks take the fewest steps (a block costs about three steps beside its query tiles),
+// the smallest on a tie: each more adds sums to write and read.  (Fewer blocks that leave SMs to dQ
+// from the start: 88 us against 63 in one sample; loads of dQ slow the block on the SM beside it.)
 int dkv_splits(int tiles, int work) {
+  if (tiles >= 148) return 1;
   int best = 1;
   int64_t best_cost = INT64_MAX;
   for (int s = 1; s <= std::min(work, 16); ++s) {
@@ -881,7 +963,7 @@ int dkv_splits(int tiles, int work) {
 
 struct BwdLayout {
   int n_pad, q_tiles, qn_tiles, kv_tiles, splits;
-  size_t lse2, delta, partial, bytes;      // offsets of the three arrays, and their end
+  size_t lse2, delta, partial, next_item, bytes;      // offsets of the arrays, and their end
 };
 
 BwdLayout bwd_layout(const CrossDims& d) {
@@ -896,8 +978,9 @@ BwdLayout bwd_layout(const CrossDims& d) {
   l.delta = stat;
   l.partial = 2 * stat;
   const int sums = l.splits == 1 ? 0 : l.splits;
-  l.bytes = l.partial +
+  l.next_item = l.partial +
             2 * static_cast<size_t>(sums) * d.B * d.Hkv * l.kv_tiles * kT * d.d * sizeof(float);
+  l.bytes = l.next_item + sizeof(int);
   return l;
 }
 
@@ -925,23 +1008,23 @@ mla_status bwd_impl(const CrossDims& d, const CrossBwdArgs& a, void* workspace, 
   float* lse2 = reinterpret_cast<float*>(ws + l.lse2);
   float* delta = reinterpret_cast<float*>(ws + l.delta);
   p.lse2 = lse2; p.delta = delta; p.partial = reinterpret_cast<float*>(ws + l.partial);
+  p.next_item = reinterpret_cast<int*>(ws + l.next_item);
   p.dev_status = a.dev_status;
   const int tiles = d.B * d.Hkv * l.kv_tiles;      // at most 2^25: a tile has a state of 64 elements
+  const int blocks = l.splits > 1 ? 148 : std::min(p.items, 148);       // (every SM takes sums)
   MLA_CUDA_TRY(cudaFuncSetAttribute(cross_dq_tc_kernel<D>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, DqShape<D>::kSmem));
   MLA_CUDA_TRY(cudaFuncSetAttribute(cross_dkv_tc_kernel<D>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, DkvShape<D>::kSmem));
   MLA_CUDA_TRY(launch_pdl(cross_stats_kernel<D>, dim3(l.n_pad / kStatRows, d.H, d.B), dim3(256), 0, s,
                           static_cast<const bf16*>(a.out), static_cast<const bf16*>(a.d_out), a.lse,
-                          lse2, delta, d.H, d.n_q, l.n_pad));
-  MLA_CUDA_TRY(launch_pdl(cross_dq_tc_kernel<D>, dim3(std::min(p.items, 148)), dim3(kThreads),
-                          DqShape<D>::kSmem, s, tq, tg, tk, tv, tdq, static_cast<bf16*>(a.d_q), p));
+                          lse2, delta, p.next_item, blocks, d.H, d.n_q, l.n_pad));
   MLA_CUDA_TRY(launch_pdl(cross_dkv_tc_kernel<D>, dim3(tiles * l.splits),
                           dim3(kThreadsKV), DkvShape<D>::kSmem, s, tqn, tgn, tk, tv,
                           static_cast<bf16*>(a.d_k), static_cast<bf16*>(a.d_v), p));
-  if (l.splits == 1) return MLA_OK;
-  MLA_CUDA_TRY(launch_pdl(cross_dkv_reduce_kernel<D>, dim3(tiles * (D / 8)),
-                          dim3(kT), 0, s, static_cast<bf16*>(a.d_k), static_cast<bf16*>(a.d_v), p));
+  MLA_CUDA_TRY(launch_pdl(cross_dq_tc_kernel<D>, dim3(blocks), dim3(kThreads), DqShape<D>::kSmem, s,
+                          tq, tg, tk, tv, tdq, static_cast<bf16*>(a.d_q), static_cast<bf16*>(a.d_k),
+                          static_cast<bf16*>(a.d_v), p));
   return MLA_OK;
 }
 

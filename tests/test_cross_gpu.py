@@ -11,9 +11,9 @@ from mla_latent_kv_attn_b200 import api, rollout
 pytestmark = pytest.mark.gpu
 
 BF16 = 2.0 ** -8
-# The tensor-core kernels round P to bf16 and may take an exponential from a polynomial that is
-# off by up to 1e-4; ex2.approx is off by 2^-22.
-P_REL = BF16 + 1.1e-4
+# The tensor-core kernels round P to bf16; ex2.approx is off by 2^-22, and so, at most, is each of the
+# two products behind a dS.
+P_REL = BF16 + 2.0 ** -20
 
 
 class Case:
@@ -346,6 +346,73 @@ def test_calls_on_two_streams_at_once():
     for c, w in zip((a, b), want):
         assert all(torch.equal(x, y) for x, y in zip(w, (c.out, c.lse, *c.grads)))
         assert int(c.status) == 0
+
+
+@pytest.mark.parametrize("shape", [
+    (1, 700, 300, 4, 4, 128, [300]),               # blocks share a tile of states: sums in dQ
+    (3, 260, 333, 8, 2, 64, [333, 0, 130]),
+    (4, 90, 300, 40, 40, 128, [300, 1, 0, 200]),   # a block per tile
+    (2, 40, 129, 3, 1, 64, [0, 0]),                # nothing to attend to
+], ids=lambda s: "x".join(map(str, s[:6])))
+def test_calls_behind_one_another_see_each_other(shape):
+    """Every launch of a chain of forward and backward calls may start before the one in front of it
+    has ended.  With one workspace, outputs written over and inputs changed between the calls, the
+    chain has to give the bits of calls that run one at a time; the chain is run eagerly and as a
+    graph."""
+    B, n_q, n_kv, H, Hkv, d, lens = shape
+    c = Case(B, n_q, n_kv, H, Hkv, d, lens=lens, seed=12)
+    steps = 6
+    inputs = [c.q.clone(), c.k.clone(), c.v.clone(), c.g.clone()]
+    results = [[torch.empty_like(t) for t in (c.out, *c.grads)] for _ in range(steps)]
+
+    def restore():
+        for t, u in zip((c.q, c.k, c.v, c.g), inputs):
+            t.copy_(u)
+        c.ws.fill_(0xFF)
+
+    def chain(wait):
+        for step in range(steps):
+            c.fwd()
+            wait()
+            c.bwd()
+            wait()
+            for to, t in zip(results[step], (c.out, *c.grads)):
+                to.copy_(t)
+            # The next inputs are this call's results: a late write or an early read would show.  (Only
+            # a part of them, or the scores grow with every step, in float64 too: to 1e10 in six, where
+            # an fp32 lse is off by 2^-24 1e10 = 600 and exp(x - lse) may be anything.)
+            c.q.copy_(c.grads[0] / 64 + inputs[0])
+            c.k.copy_(c.grads[1] / 64 + inputs[1])
+            c.v.copy_(c.grads[2] / 64 + inputs[2])
+            c.g.copy_(c.out / 64 + inputs[3])
+            wait()
+
+    restore()
+    chain(torch.cuda.synchronize)
+    want = [[t.clone() for t in r] for r in results]
+    assert all(torch.isfinite(t).all() for r in want for t in r)
+
+    def check():
+        torch.cuda.synchronize()
+        assert int(c.status) == 0
+        for got, ref in zip(results, want):
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
+            for t in got:
+                t.fill_(7.0)
+
+    for _ in range(5):
+        restore()
+        chain(lambda: None)
+        check()
+    restore()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        chain(lambda: None)
+    for _ in range(5):
+        restore()
+        graph.replay()
+        check()
 
 
 def test_bad_pointers_are_refused():
