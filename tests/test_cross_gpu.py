@@ -415,6 +415,47 @@ def test_calls_behind_one_another_see_each_other(shape):
         check()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_arrays_of_almost_2_to_31_elements(d):
+    """Rows whose byte offsets (and, for 64-bit reads of the arrays, element offsets) are near the
+    largest allowed.  Only the first and the last 64 queries have an upstream gradient, so dK and dV
+    are those of a call with these 128 queries alone; the others' dQ is exactly zero."""
+    H, n_kv, ends = 12, 70, 64
+    n_q = (2 ** 31 - 1) // (H * d) - 1
+    n_q -= n_q % 80 - 17                       # a ragged last tile
+    small = Case(1, 2 * ends, n_kv, H, 3, d, seed=3)
+    small.fwd()
+    small.bwd()
+    small.check()
+    c = Case(1, 1, n_kv, H, 3, d)              # (a config and buffers to widen)
+    cc = api.make_cross_config(batch=1, n_heads=H, n_kv_heads=3, d_head=d, n_q=n_q, n_kv=n_kv)
+    new = lambda: torch.zeros((1, n_q, H, d), device="cuda", dtype=torch.bfloat16)
+    q, g, out, d_q = new(), new(), new(), new().fill_(7.0)
+    lse = torch.zeros((1, H, n_q), device="cuda")
+    pick = lambda t: torch.cat((t[:, :ends], t[:, -ends:]), 1)
+    for big, part in ((q, small.q), (g, small.g)):
+        big[:, :ends], big[:, -ends:] = part[:, :ends], part[:, ends:]
+    api.mla_cross_attention_fwd(cc, q, small.k, small.v, out, lse=lse, dev_status=c.status)
+    ws = torch.empty(api.mla_cross_attention_bwd_workspace_bytes(cc), device="cuda",
+                     dtype=torch.uint8)
+    d_k, d_v = torch.empty_like(small.k), torch.empty_like(small.v)
+    api.mla_cross_attention_bwd(cc, q, small.k, small.v, out, lse, g, d_q, d_k, d_v, ws,
+                                dev_status=c.status)
+    assert int(c.status) == 0
+    # a row's results take no part of other rows (one tile of states or one rescaling rule a warp
+    # apart: within two roundings to bf16)
+    for got, want in ((pick(out), small.out), (pick(d_q), small.grads[0])):
+        err = (got.float() - want.float()).abs()
+        assert (err <= 2 * BF16 * want.float().abs() + 1e-5).all()
+    assert (pick(lse.transpose(1, 2)) - small.lse.transpose(1, 2)).abs().max() <= 2.0 ** -20
+    assert (d_q[:, ends:-ends] == 0).all()
+    # the same 128 terms in fp32, summed in another order: 128 roundings of 2^-24 of the terms' sum of
+    # magnitudes, below 2^-10 here, and one rounding to bf16 each
+    for got, want in ((d_k, small.grads[1]), (d_v, small.grads[2])):
+        err = (got.float() - want.float()).abs()
+        assert (err <= 2 * BF16 * want.float().abs() + 2.0 ** -10).all()
+
+
 def test_bad_pointers_are_refused():
     c = Case(1, 8, 16, 2, 2, 64)
     host = torch.zeros(c.q.shape, dtype=c.dt)

@@ -374,6 +374,28 @@ def test_host_streamer_serves_4_bit_rings():
         assert torch.equal(served[r].scales, rings[r].scales), r
 
 
+def test_ring_of_almost_2_to_31_values():
+    """Appending to the last slots of the largest ring, and its values read back."""
+    cfg = dataclasses.replace(inputs.CONFIGS[1], window_frames=(2 ** 31 - 1) // (1560 * 224) - 1)
+    c = api.make_config(cfg)
+    tpf, W, C = cfg.tokens_per_frame, cfg.window_frames, cfg.chunk_frames
+    ring = rollout.RingQ4(c)
+    lat = _chunk(c, 4)
+    first = 2 * W - C                               # the window's last slots, once around
+    _append(c, ring, lat, first)
+    small = dataclasses.replace(cfg, window_frames=C)
+    cs = api.make_config(small)
+    want = rollout.RingQ4(cs)
+    _append(cs, want, lat, 0)
+    assert torch.equal(ring.codes[:, -C * tpf:], want.codes)
+    assert torch.equal(ring.scales[:, -C * tpf:], want.scales)
+    assert ring.slot_frame[0, -C:].tolist() == list(range(first, first + C))
+    assert (ring.slot_frame[0, :-C] == -1).all() and (ring.codes[:, :-C * tpf] == 0x88).all()
+    values = ring.read()
+    assert torch.equal(values[:, -C * tpf:], want.read())
+    assert not values[:, :-C * tpf].any()
+
+
 def test_prefill_on_a_side_stream():
     cfg = SMALL
     c = api.make_config(cfg)
