@@ -19,9 +19,9 @@
 // traffic than the two products (115 MB for 4680 queries, 12 heads and 512 states).
 // (The statistics inside the dQ kernel, by warps of their own, made that call 75 us instead of 70: the
 // first tiles wait for rows from DRAM.)
-// Measured: 4680 queries, 512 states, 12 heads of 128: 63 us a call with inputs in L2, 585 TFLOP/s over
+// Measured: 4680 queries, 512 states, 12 heads of 128: 63 us a call (three inputs in turn), 585 TFLOP/s over
 // the five products of the formula and 819 over the seven computed (0.50 of the measured peak), 69 us
-// with inputs in memory; batch 4 with mixed lengths 180 to 197 us; batch 2, 1333 queries, up to 333
+// where every call finds its inputs in memory; batch 4 with mixed lengths 180 to 197 us; batch 2, 1333 queries, up to 333
 // states, 16 heads of 64 on 4: 34 us.
 // P and dS are rounded to bf16 as operands (in TMEM); every product accumulates in fp32 in TMEM.
 // Every wait is bounded; one that runs out writes MLA_ERR_DEVICE_TIMEOUT to dev_status.
@@ -279,7 +279,8 @@ __device__ __forceinline__ DqItem dq_item(const CrossBwdParams& p, int it) {
 
 // Roles (384 threads): warps 0-7 softmax (warps w and w + 4 share 32 rows, each half of the
 // columns), 8 TMA producer, 9 issuer of S, 10 issuer of dP and dQ, 11 sums of dK and dV, which
-// the softmax warps end after their items.  The two dP buffers let dP(j+1) run under the softmax of j, and S(j+1) runs once S(j) has been read.
+// the softmax warps end after their items.  The two dP buffers let dP(j+1) run under the softmax of
+// j, and S(j+1) runs once S(j) has been read.
 // The producer draws the block's items after its first from a counter that the statistics reset, an
 // item ahead of its loads, and hands them to the other roles; these take an item ahead of their work
 // (the softmax reads its rows' statistics then).  Blocks start as the dK, dV kernel's end and lengths
