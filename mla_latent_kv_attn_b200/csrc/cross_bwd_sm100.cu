@@ -19,10 +19,10 @@
 // traffic than the two products (115 MB for 4680 queries, 12 heads and 512 states).
 // (The statistics inside the dQ kernel, by warps of their own, made that call 75 us instead of 70: the
 // first tiles wait for rows from DRAM.)
-// Measured: 4680 queries, 512 states, 12 heads of 128: 63 us a call (three inputs in turn), 585 TFLOP/s over
-// the five products of the formula and 819 over the seven computed (0.50 of the measured peak), 69 us
-// where every call finds its inputs in memory; batch 4 with mixed lengths 180 to 197 us; batch 2, 1333 queries, up to 333
-// states, 16 heads of 64 on 4: 34 us.
+// Measured: 4680 queries, 512 states, 12 heads of 128: 63 us a call (three inputs in turn), 585 TFLOP/s
+// over the five products of the formula and 819 over the seven computed (0.50 of the measured peak),
+// 69 us where every call finds its inputs in memory; batch 4 with mixed lengths 180 to 197 us; batch
+// 2, 1333 queries, up to 333 states, 16 heads of 64 on 4: 34 us.
 // P and dS are rounded to bf16 as operands (in TMEM); every product accumulates in fp32 in TMEM.
 // Every wait is bounded; one that runs out writes MLA_ERR_DEVICE_TIMEOUT to dev_status.
 #include "cross_tc.cuh"
