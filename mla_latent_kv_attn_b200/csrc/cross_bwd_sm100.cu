@@ -256,7 +256,8 @@ struct DqShared {
   uint64_t v_full[kVStages], v_empty[kVStages];
   uint64_t s_full, s_free;                // S(j) complete; read
   uint64_t dp_full[2], dq_done[2];        // dP(j) complete; the product with dS(j) complete
-  uint64_t ds_full;                       // dS(j) in TMEM
+  uint64_t ds_full[2];                    // dS(j) in TMEM: by parity, for dS(j+1) may come before
+                                          // the issuer has seen dS(j)
   uint64_t acc_free;                      // the item's dQ is in registers
   uint64_t staged, stage_free;            // and in shared memory; stored from there
   uint32_t tmem_base;
@@ -317,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sh.dp_full[b]), 1);
       mbar_init(smem_u32(&sh.dq_done[b]), 1);
+      mbar_init(smem_u32(&sh.ds_full[b]), kSoftmaxThreads);
     }
     for (int s = 0; s < kItems; ++s) {
       mbar_init(smem_u32(&sh.item_full[s]), 1);
@@ -332,7 +334,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&sh.s_full), 1);
     mbar_init(smem_u32(&sh.s_free), kSoftmaxThreads);
-    mbar_init(smem_u32(&sh.ds_full), kSoftmaxThreads);
     mbar_init(smem_u32(&sh.acc_free), kSoftmaxThreads);
     mbar_init(smem_u32(&sh.staged), kSoftmaxThreads);
     fence_barrier_init();
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait(sh.g_full, n) && issue_dp(t, nt == 1);
         for (int j = 0; j < nt && ok; ++j, ++t) {
           if (j + 1 < nt) ok = issue_dp(t + 1, j + 2 == nt);
-          ok = ok && wait(sh.ds_full, t) && (j > 0 || n == 0 || wait(sh.acc_free, n - 1));
+          ok = ok && wait(sh.ds_full[t & 1], t >> 1) && (j > 0 || n == 0 || wait(sh.acc_free, n - 1));
           if (!ok) break;
           tc_fence_after();
           mma_pairs_by_tile<D>(tmem + kDqColAcc, tmem + kDqColDP + 128 * (t & 1),
@@ -563,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_u32(&sh.ds_full));
+        mbar_arrive(smem_u32(&sh.ds_full[t & 1]));
       }
       if (!ok) break;
       if (threadIdx.x == 0 && n > 0) {       // its copy out of shared memory, an item ago
