@@ -90,7 +90,8 @@ struct FwdShared {
   uint64_t p_full[2][2];     // each half of the states of P(j) is in TMEM
   uint64_t pv_done[2];       // PV(j) complete
   uint64_t o_free[2];        // the item's O is in registers
-  uint64_t o_staged[2];      // and in the item's Q buffer
+  uint64_t o_staged[2][2];   // and in the item's Q buffer: by buffer, for the next item's O may come
+                             // before the store warp has seen this one's
   uint64_t first_qk[2];      // stream 0's first S of an item (by parity)
   uint32_t tmem_base;
   int abort_flag;
@@ -220,12 +221,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&q_full[i][b]), 1);
         mbar_init(smem_u32(&q_empty[i][b]), 1);
         mbar_init(smem_u32(&p_full[i][b]), kStreamThreads);
+        mbar_init(smem_u32(&o_staged[i][b]), kStreamThreads);
       }
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&s_free[i]), kStreamThreads);
       mbar_init(smem_u32(&pv_done[i]), 1);
       mbar_init(smem_u32(&o_free[i]), kStreamThreads);
-      mbar_init(smem_u32(&o_staged[i]), kStreamThreads);
       mbar_init(smem_u32(&first_qk[i]), 1);
     }
     for (int s = 0; s < kStages; ++s) {
@@ -305,9 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         next = decode(it + item_step);
         if (w.nt == 0) continue;
         for (int i = 0; i < w.streams; ++i) {
-          ok = wait(o_staged[i], n_item[i]);
+          const int b = n_item[i] & 1;
+          ok = wait(o_staged[i][b], n_item[i]++ >> 1);
           if (!ok) break;
-          const int b = n_item[i]++ & 1;
           for (int k = 0; k < Sh::kBlocks; ++k)     // (rows past n_q are not written)
             tma_store_4d(&tm_o, sQ + (2 * i + b) * kTile + k * kBlk, 64 * k, w.h, w.q0 + i * kBM,
                          w.b);
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(smem_u32(&o_free[i]));
       fence_proxy_async_smem();
-      mbar_arrive(smem_u32(&o_staged[i]));
+      mbar_arrive(smem_u32(&o_staged[i][n_item & 1]));
       ++n_item;
     }
   }

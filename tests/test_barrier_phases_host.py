@@ -126,7 +126,43 @@ def test_gradient_of_the_queries(tiles):
     assert dq_roles(tiles, arrays).explore() is None
 
 
+def store_roles(items, arrays):
+    """cross_fwd_tc_kernel's hand-over of O to the warp that stores it: items of one or two streams,
+    two softmax threads each.  K and V of an item are loaded behind its Q tiles."""
+    r = Roles({})
+    producer, store = r.role("producer"), r.role("store")
+    count = [0, 0]
+    for n, streams in enumerate(items):
+        for i in range(streams):
+            c = count[i]
+            buf = f"[{i}][{c & 1}]"
+            if c >= 2:
+                producer.append(("wait", "q_empty" + buf, (c >> 1) - 1))
+            staged = (f"o_staged{buf}", c >> 1) if arrays else (f"o_staged[{i}]", c)
+            r.counts.update({staged[0]: 2, f"o_free[{i}]": 2})
+            store.extend([("wait", *staged), ("arrive", "q_empty" + buf, c >> 1)])
+            issuer = r.role(f"issuer {i}")
+            issuer.append(("take", f"loads {i}"))
+            if c > 0:
+                issuer.append(("wait", f"o_free[{i}]", c - 1))
+            issuer.append(("arrive", f"pv_done[{i}]", c))
+            for x in range(2):
+                r.role(f"x{i}{x}").extend([("wait", f"pv_done[{i}]", c),
+                                           ("arrive", f"o_free[{i}]", c), ("arrive", *staged)])
+            count[i] += 1
+        for i in range(streams):
+            producer.append(("post", f"loads {i}"))
+    return r
+
+
+@pytest.mark.parametrize("items", [[2, 2, 2, 2], [1, 1, 1, 1, 1], [2, 2, 1, 1]], ids=str)
+def test_stores_of_the_forward(items):
+    arrays = declared("cross_sm100.cu", "FwdShared", "o_staged") == ["2", "2"]
+    assert store_roles(items, arrays).explore() is None
+
+
 def test_a_single_barrier_misses_a_phase():
     """The explorer finds what it is for: with one barrier for every use, arrivals for a phase come
     while the one before it is open."""
     assert dq_roles([3], False).explore() is not None
+    assert store_roles([2, 2, 2], False).explore() is not None
