@@ -30,7 +30,8 @@
 // registers and frees the buffer at once, so QK(j+1) overlaps the softmax of j; P has its own
 // buffer for the same reason.
 // With DC = 256 O and P leave no room for Q: Q stays in shared memory, there are two S buffers,
-// P(j) is written into S buffer j&1 and QK(j+2) waits for PV(j).
+// P(j) is written into S buffer j&1 and QK(j+2) waits for PV(j).  A softmax warp may then hand over
+// P(j+1) before another has handed over P(j), so each buffer has barriers of its own.
 //
 // kHalf: the same kernel with fp16 operands in place of bf16, for keys and values that fp16 holds
 // exactly or nearly so (the 4-bit ring's, ring_q4.cu).  fp16 has three bits more at the same rate:
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t kv_empty[kStages];
   __shared__ __align__(8) uint64_t s_full[2];
   __shared__ __align__(8) uint64_t s_free[2];
-  __shared__ __align__(8) uint64_t p_full;
+  __shared__ __align__(8) uint64_t p_full[kAliasP ? 2 : 1];
   __shared__ __align__(8) uint64_t pv_done;
   __shared__ __align__(8) uint64_t pv_buf_done[2];   // PV(j) done, per S buffer (aliased P)
   __shared__ __align__(8) uint64_t w_full;
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&s_free[i]), kSoftmaxThreads);
     }
-    mbar_init(smem_u32(&p_full), kSoftmaxThreads);
+    for (uint64_t& bar : p_full) mbar_init(smem_u32(&bar), kSoftmaxThreads);
     mbar_init(smem_u32(&pv_done), 1);
     mbar_init(smem_u32(&pv_buf_done[0]), 1);
     mbar_init(smem_u32(&pv_buf_done[1]), 1);
@@ -534,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         for (int j = 0; j < p.nt && ok; ++j) {
-          ok = wait_bar(smem_u32(&p_full), j & 1, abort_flag, p.dev_status);
+          ok = wait_bar(smem_u32(&p_full[kAliasP ? j & 1 : 0]), (kAliasP ? j >> 1 : j) & 1, abort_flag,
+                        p.dev_status);
           if (!ok) break;
           tc_fence_after();
           const int s = (nqc + j) % kStages;
@@ -715,11 +717,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(smem_u32(&p_full));
+      mbar_arrive(smem_u32(&p_full[kAliasP ? j & 1 : 0]));
     }
-    if (ok)
+    if (ok) {
+      // (an aliased P: PV(nt-2) may not be complete yet, so PV(nt-1) by its buffer's barrier)
+      const int last = p.nt - 1;
+      const uint32_t bar = smem_u32(kAliasP ? &pv_buf_done[last & 1] : &pv_done);
       ok = __all_sync(0xffffffffu,
-                      wait_bar(smem_u32(&pv_done), (p.nt - 1) & 1, abort_flag, p.dev_status));
+                      wait_bar(bar, (kAliasP ? last >> 1 : last) & 1, abort_flag, p.dev_status));
+    }
     if (ok) {
       tc_fence_after();
       const float inv_l = 1.f / l_run;

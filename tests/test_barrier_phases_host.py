@@ -14,12 +14,11 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "mla_latent_kv_attn_b200", "csrc")
 
 
-def declared(source, struct, name):
-    """The extents of barrier array `name` in `struct` (empty for a single barrier)."""
-    text = open(os.path.join(CSRC, source)).read()
-    body = text.split(f"struct {struct} {{", 1)[1].split("\n};", 1)[0]
-    m = re.search(rf"uint64_t (?:[^;]*, )?{name}((?:\[\w+\])*)[,;]", body)
-    return re.findall(r"\[(\w+)\]", m.group(1))
+def declared(source, start, name):
+    """The extents of barrier array `name`, declared behind `start` (empty for a single barrier)."""
+    body = open(os.path.join(CSRC, source)).read().split(start, 1)[1]
+    m = re.search(rf"uint64_t (?:[^;]*, )?{name}((?:\[[^\]]+\])*)[,;]", body)
+    return re.findall(r"\[([^\]]+)\]", m.group(1))
 
 
 class Roles:
@@ -122,7 +121,7 @@ def dq_roles(tiles, ds_arrays):
 
 @pytest.mark.parametrize("tiles", [[5], [1, 1, 1, 1], [3, 2], [2, 1, 3]], ids=str)
 def test_gradient_of_the_queries(tiles):
-    arrays = declared("cross_bwd_sm100.cu", "DqShared", "ds_full") == ["2"]
+    arrays = declared("cross_bwd_sm100.cu", "struct DqShared {", "ds_full") == ["2"]
     assert dq_roles(tiles, arrays).explore() is None
 
 
@@ -157,8 +156,41 @@ def store_roles(items, arrays):
 
 @pytest.mark.parametrize("items", [[2, 2, 2, 2], [1, 1, 1, 1, 1], [2, 2, 1, 1]], ids=str)
 def test_stores_of_the_forward(items):
-    arrays = declared("cross_sm100.cu", "FwdShared", "o_staged") == ["2", "2"]
+    arrays = declared("cross_sm100.cu", "struct FwdShared {", "o_staged") == ["2", "2"]
     assert store_roles(items, arrays).explore() is None
+
+
+def aliased_p_roles(nt, arrays, rescale):
+    """attention_tc_kernel with P in the S buffers (256 content latents): two softmax warps, of which
+    those in `rescale` wait for the product before each tile's."""
+    r = Roles({f"p_full[{i}]": 2 for i in range(2)} | {"p_full": 2})
+    qk, pv = r.role("issuer QK"), r.role("issuer PV")
+    tqk, tpv = r.role("tensor QK"), r.role("tensor PV")
+    s_full, buf_done = by_parity("s_full", True), by_parity("pv_buf_done", True)
+    p_full = by_parity("p_full", arrays)
+    for j in range(nt):
+        if j >= 2:
+            qk.append(("wait", *buf_done(j - 2)))
+        qk.append(("post", "QK"))
+        tqk.extend([("take", "QK"), ("arrive", *s_full(j))])
+        pv.extend([("wait", *p_full(j)), ("post", "PV")])
+        tpv.extend([("take", "PV"), ("arrive", "pv_done", j), ("arrive", *buf_done(j))])
+    for x in range(2):
+        steps = r.role(f"x{x}")
+        for j in range(nt):
+            steps.append(("wait", *s_full(j)))
+            if x in rescale and j > 0:
+                steps.append(("wait", "pv_done", j - 1))
+            steps.append(("arrive", *p_full(j)))
+        steps.append(("wait", *(buf_done(nt - 1) if arrays else ("pv_done", nt - 1))))
+    return r
+
+
+@pytest.mark.parametrize("rescale", [(), (0,), (0, 1)], ids=str)
+@pytest.mark.parametrize("nt", [1, 2, 3, 6])
+def test_probabilities_in_the_score_buffers(nt, rescale):
+    arrays = declared("attention_sm100.cu", "attention_tc_kernel(", "p_full") == ["kAliasP ? 2 : 1"]
+    assert aliased_p_roles(nt, arrays, rescale).explore() is None
 
 
 def test_a_single_barrier_misses_a_phase():
@@ -166,3 +198,4 @@ def test_a_single_barrier_misses_a_phase():
     while the one before it is open."""
     assert dq_roles([3], False).explore() is not None
     assert store_roles([2, 2, 2], False).explore() is not None
+    assert aliased_p_roles(3, False, ()).explore() is not None
