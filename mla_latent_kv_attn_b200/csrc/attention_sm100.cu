@@ -40,6 +40,8 @@
 // a power of two that brings its largest element to 2^14 .. 2^15, and the row's scores are scaled
 // back; P stays below 2^8.  The latent output meets W_UV (bf16) as the sum of two bf16 numbers,
 // both from TMEM, instead of one: 12 products more in an epilogue, and no rounding of it.
+#include <cfloat>
+
 #include "exp2.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -623,6 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(smem_u32(&q_full));
     }
+    // A row of zeros or of the least numbers under a small scale: the product would be 0, and a masked
+    // score, -infinity, times 0 a NaN.  Scores stay below 2^40, so under the least normal number they
+    // are nothing, as they are under what it stands for.
+    if constexpr (kHalf) row_scale_log2 = fmaxf(row_scale_log2, FLT_MIN);
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < p.nt; ++j) {

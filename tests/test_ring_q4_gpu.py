@@ -223,6 +223,42 @@ def test_attention_from_cq_matches_the_definition(d_c, d_rope, chunks):
     assert np.linalg.norm(err) <= 1e-5 * np.linalg.norm(lse)
 
 
+@pytest.mark.parametrize("scale", [1e-8, 1e-30, 1e-42])
+@pytest.mark.parametrize("d_c,d_rope,from_cq", [(192, 32, False), (256, 32, False), (192, 32, True)])
+def test_rows_of_zeros_and_the_smallest_scales(d_c, d_rope, from_cq, scale):
+    """Scores of nothing: rows of zeros, of the least numbers and ordinary ones under scales down to
+    fp32's subnormal ones weigh every key alike, in tiles with masked columns too."""
+    cfg = dataclasses.replace(inputs.with_latent_shape(SMALL, d_c, d_rope), n_heads=2)
+    c, q4, plain = _filled(cfg, api.MLA_PATH_AUTO, 2)
+    first, n_valid = rollout.chunk_schedule(cfg.chunk_frames, cfg.window_frames, 2)
+    lat, (q, w_uv) = _chunk(c, 100), _query(c, 101)
+    c.softmax_scale = scale
+    b = rollout.ChunkBuffers(c, q4=True)
+    ring = (lat, q4.codes, q4.scales, q4.slot_frame, n_valid, first, w_uv, b.o, b.lse, b.workspace,
+            b.dev_status)
+    if from_cq:
+        g = torch.Generator(device="cuda").manual_seed(7)
+        c_q = torch.randn((cfg.batch, cfg.n_q, c.d_cq), generator=g, device="cuda").bfloat16()
+        w_q = (torch.randn((c.n_heads, cfg.d_latent, c.d_cq), generator=g, device="cuda")
+               * c.d_cq ** -0.5).bfloat16()
+        c_q[:, ::3] = 0
+        c_q[:, 1::3] *= 2.0 ** -120
+        api.mla_attention_fwd_from_cq_q4(c, c_q, w_q, *ring)
+        q = torch.einsum("bnk,hdk->bnhd", c_q.double(), w_q.double())    # (its rotation is nothing here)
+    else:
+        q[:, ::3] = 0
+        q[:, 1::3] *= 2.0 ** -128
+        api.mla_attention_fwd_q4(c, q, *ring)
+    torch.cuda.synchronize()
+    rollout.check_device_status(b)
+    seen = to_np(q).astype(np.float64) * (c.softmax_scale / cfg.softmax_scale)
+    out, lse, e_out, e_lse = _reference(c, cfg, to_np(plain.cache), plain.slot_frame.cpu().numpy(),
+                                        to_np(lat), seen, F16 * np.abs(seen), to_np(w_uv), first,
+                                        n_valid)
+    _within(b.o.view(*q.shape[:3], -1), out, e_out, 2.0 ** -8)
+    _within(b.lse, lse, e_lse, 0.0)
+
+
 def test_chunk_latents_beyond_fp16():
     """The chunk's own latents enter the tensor-core attention held at fp16's limits; the ring holds
     no more than 26880 in any case."""
