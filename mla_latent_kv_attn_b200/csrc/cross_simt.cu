@@ -15,6 +15,8 @@
 // twice; with the elements over the lanes in both, a butterfly sum per row and four rows in flight
 // bounded these kernels (16 queries against 24 states in fp32: 14.3 us a call, now bound by the
 // launch).  All sums are fp32 and run in a fixed order.
+#include <cfloat>
+
 #include "cross.h"
 
 namespace mla {
@@ -108,12 +110,12 @@ __global__ void __launch_bounds__(32 * kWarps)
   const T* v0 = static_cast<const T*>(a.v) + static_cast<int64_t>(b) * d.n_kv * d.v_row +
                 static_cast<int64_t>(kh) * d.d;
   float o[kPer] = {};
-  float m = -INFINITY, l = 0.f;
+  float m = -FLT_MAX, l = 0.f;          // (finite: scores of -infinity weigh nothing)
   for (int j0 = 0; j0 < len; j0 += 32) {
     const int n = min(32, len - j0);
     const float x = lane < n ? dot_row<T, kVec>(k0 + (j0 + lane) * d.k_row, mine, d.d) * scale_log2
                              : -INFINITY;
-    const float mn = fmaxf(m, warp_max(x));       // (lane 0 has a score)
+    const float mn = fmaxf(m, warp_max(x));
     const float alpha = exp2f(m - mn), p = exp2f(x - mn);
     m = mn;
     l = l * alpha + warp_sum(p);

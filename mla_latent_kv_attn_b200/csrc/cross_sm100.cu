@@ -28,6 +28,8 @@
 // peak; 2.5 rounds of items, and the products' hand-overs bound each); batch 2, 1333 queries, up to
 // 1501 states, 16 heads of 64 on 4: 42 us, bound by the exponentials (35.5 without them); one query:
 // 9.3 us, the host's side of the call.
+#include <cfloat>
+
 #include "cross_tc.cuh"
 
 namespace mla {
@@ -440,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         bool rescale = false;
         if (j == 0) {
-          m = mx;
+          m = fmaxf(mx, -FLT_MAX);      // scores of -infinity weigh nothing, also in the first tile
         } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
           const float m_new = fmaxf(m, mx);
           alpha = fast_exp2(m - m_new);

@@ -181,6 +181,43 @@ def test_rising_scores_move_the_maximum_in_every_tile(d):
     c.check()
 
 
+@pytest.mark.parametrize("first", [130, 300])
+@pytest.mark.parametrize("n_q", [5, 2500])
+@pytest.mark.parametrize("key", [-2.0 ** 66, -float("inf")])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (16, "bf16"), (40, "fp32")])
+def test_first_states_below_every_score(d, dtype, key, n_q, first):
+    """Scores of the first tiles that are -infinity, or overflow to it, weigh nothing; the rest is the
+    call on the states behind them, however the states are split over blocks.  (With infinite keys dQ,
+    a sum of 0 * infinity, is no number by its definition either.)"""
+    c = Case(2, n_q, 400, 4, 2, d, lens=[400, 350], dtype=dtype, scale=0.25, seed=8)
+    c.q[..., 0] = 2.0 ** 64
+    c.k[..., 0] *= 2.0 ** -64
+    c.k[:, :first, :, 0] = key                     # 2^64 2^66 / 4 is 2^128
+    c.fwd()
+    if np.isfinite(key):
+        c.bwd()
+    part = object.__new__(Case)
+    part.__dict__.update(c.__dict__)
+    part.cc = api.make_cross_config(batch=2, n_heads=4, n_kv_heads=2, d_head=d, n_q=n_q,
+                                    n_kv=400 - first, softmax_scale=0.25, dtype=dtype)
+    part.lens = [400 - first, 350 - first]
+    part.k, part.v = c.k[:, first:], c.v[:, first:]
+    part.grads = [c.grads[0], *(t[:, first:] for t in c.grads[1:])]
+    part.check(backward=np.isfinite(key))
+    if np.isfinite(key):
+        assert all((t[:, :first] == 0).all() for t in c.grads[1:])
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (40, "fp32")])
+def test_the_smallest_scales_weigh_every_state_alike(d, dtype):
+    for n_q in (3, 300):
+        c = Case(2, n_q, 100, 2, 1, d, lens=[100, 41], dtype=dtype, scale=1e-42)
+        c.q[:, ::2] = 0
+        c.fwd()
+        c.bwd()
+        c.check()
+
+
 @pytest.mark.parametrize("d", [16, 64, 128])
 def test_same_call_same_bits_and_no_writes_outside(d):
     c = Case(2, 150, 260, 6, 2, d, lens=[260, 101])
