@@ -12,6 +12,7 @@ first min(frames so far, W) slots are exactly the filled ones and attention walk
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import Optional, Tuple
 
@@ -25,6 +26,18 @@ def chunk_schedule(chunk_frames: int, window_frames: int, chunk: int) -> Tuple[i
     """(first_frame, n_valid_frames) of a chunk."""
     first = chunk * chunk_frames
     return first, min(first, window_frames)
+
+
+def _allocating_on(stream):
+    """Tensors made in this context belong to `stream` (a call's argument: None, a stream or a raw
+    handle).  From the current stream's pool they could be memory that work queued there still uses,
+    and nothing orders `stream` behind that work."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else \
+            torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 @dataclasses.dataclass
@@ -89,9 +102,11 @@ class RingQ4:
                                      dtype=torch.int32)
 
     def read(self, stream=None) -> torch.Tensor:
-        """The ring's values [B, W*tpf, D], as a Ring's cache holds them."""
-        out = torch.empty((*self.codes.shape[:2], self.c.d_c + self.c.d_rope),
-                          device=self.codes.device, dtype=api.torch_dtype(self.c))
+        """The ring's values [B, W*tpf, D], as a Ring's cache holds them; they belong to the stream
+        that the call runs on."""
+        with _allocating_on(stream):
+            out = torch.empty((*self.codes.shape[:2], self.c.d_c + self.c.d_rope),
+                              device=self.codes.device, dtype=api.torch_dtype(self.c))
         api.mla_cache_read_q4(self.c, self.codes, self.scales, out, stream=stream)
         return out
 
@@ -489,7 +504,7 @@ class EncoderStates:
     per sample, kv_len [B] (None: all).  attend() is the layer's cross attention, backward() its
     gradients.  The backward's workspaces (one per size asked for) belong to the object and stay as
     long as it does, for graphs that captured them; so the backward calls of one object are ordered
-    on one stream."""
+    on one stream, for which their workspaces are allocated."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, n_heads: int,
                  kv_len: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None):
@@ -516,7 +531,8 @@ class EncoderStates:
         cc = self.config(q.shape[1])
         need = api.mla_cross_attention_bwd_workspace_bytes(cc)
         if need not in self.workspaces:
-            self.workspaces[need] = torch.empty((need,), device=q.device, dtype=torch.uint8)
+            with _allocating_on(stream):
+                self.workspaces[need] = torch.empty((need,), device=q.device, dtype=torch.uint8)
         api.mla_cross_attention_bwd(cc, q, self.k, self.v, out, lse, d_out, d_q, d_k, d_v,
                                     self.workspaces[need], kv_len=self.kv_len,
                                     dev_status=self.dev_status, stream=stream)

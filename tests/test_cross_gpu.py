@@ -330,6 +330,25 @@ def test_encoder_states_serve_chunks_and_training():
     assert int(e.dev_status) == 0
 
 
+def test_encoder_states_on_a_side_stream():
+    """The workspace that a backward call makes is memory of the stream it runs on: a block just freed
+    on the current stream, behind work that has yet to read and write it, is not taken."""
+    c = Case(2, 60, 300, 4, 2, 128, lens=[300, 20])
+    e = rollout.EncoderStates(c.k, c.v, n_heads=4, kv_len=c.kv_len)
+    side = torch.cuda.Stream()
+    block = torch.full_like(c.ws, 5)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                          # some 50 ms on the current stream
+    kept = block.clone()
+    block.fill_(0x7F)
+    del block
+    e.attend(c.q, c.out, lse=c.lse, stream=side)
+    e.backward(c.q, c.out, c.lse, c.g, *c.grads, stream=side)
+    torch.cuda.synchronize()
+    c.check()
+    assert (kept == 5).all() and int(e.dev_status) == 0
+
+
 def test_layer_sized_call():
     """A chunk of the Wan-shaped layer against prompts of two lengths: every element of the first and
     the last head (whose keys no other head shares) against the definition."""

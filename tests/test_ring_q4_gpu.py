@@ -450,6 +450,25 @@ def test_prefill_on_a_side_stream():
     assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_read_on_a_side_stream(raw):
+    """The values are written into memory of the stream that writes them: a block just freed on the
+    current stream, behind work that has yet to read and write it, is not taken."""
+    c, ring, _ = _filled(SMALL, api.MLA_PATH_AUTO, 2)
+    want = ring.read()
+    side = torch.cuda.Stream()
+    block = torch.full_like(want, 5.0)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                          # some 50 ms on the current stream
+    kept = block.clone()
+    block.fill_(7.0)
+    del block
+    got = ring.read(stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert (kept == 5.0).all()
+
+
 def test_bad_calls_are_refused():
     c, q4, _ = _filled(SMALL, api.MLA_PATH_AUTO, 1)
     buf = rollout.ChunkBuffers(c, q4=True)
