@@ -42,10 +42,11 @@ struct CrossBwdArgs {
   int32_t* dev_status;
 };
 
-// Valid states of sample b: kv_len[b] clamped to [0, n_kv].
+// Valid states of sample b: kv_len[b] clamped to [0, n_kv].  (From L2: some kernels read it before they
+// wait for the grid in front of them.)
 __device__ __forceinline__ int cross_len(const int32_t* kv_len, int b, int n_kv) {
   if (kv_len == nullptr) return n_kv;
-  const int n = kv_len[b];
+  const int n = __ldcg(kv_len + b);
   return n < 0 ? 0 : (n > n_kv ? n_kv : n);
 }
 

@@ -288,7 +288,9 @@ __device__ __forceinline__ DqItem dq_item(const CrossBwdParams& p, int it) {
 // differ: with a fixed share for each block, the call of four samples took 216 us.
 // (Three more warps for the sums would leave each thread 128 registers, too few for the softmax.)
 // This grid starts block by block as the dK, dV kernel's blocks end: only the sums need its results.
-// (It starts when every block of that kernel runs and has seen the end of the statistics.)
+// (It starts when every block of that kernel runs and has seen the end of the statistics.  What it
+// reads before its own wait comes from L2, where everything written before the statistics ended is:
+// this SM's L1 may hold lines from before.)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -505,8 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto read_stats = [&]() {
       if (next.q0 < 0) return;
       const int64_t at = (static_cast<int64_t>(next.b) * p.H + next.h) * p.n_pad + next.q0 + row;
-      next_l = p.lse2[at];
-      next_d = p.delta[at];
+      next_l = __ldcg(p.lse2 + at);
+      next_d = __ldcg(p.delta + at);
     };
     read_stats();
     while (ok && next.q0 >= 0) {

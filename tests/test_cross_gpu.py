@@ -472,6 +472,53 @@ def test_calls_behind_one_another_see_each_other(shape):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+def test_lengths_and_inputs_rewritten_between_calls(d):
+    """Small calls in one chain, eager and as a graph, with the lengths, the inputs and the workspace's
+    statistics rewritten between them: each call sees what was written just before it."""
+    c = Case(3, 40, 200, 2, 2, d, lens=[200, 200, 200], seed=13)
+    steps = 12
+    g = torch.Generator(device="cuda").manual_seed(14)
+    lens = torch.randint(0, 201, (steps, 3), generator=g, device="cuda", dtype=torch.int32)
+    qs = torch.randn((steps, *c.q.shape), generator=g, device="cuda").to(c.dt)
+    results = [[torch.empty_like(t) for t in (c.out, c.lse, *c.grads)] for _ in range(steps)]
+
+    def chain(wait):
+        for step in range(steps):
+            c.kv_len.copy_(lens[step])
+            c.q.copy_(qs[step])
+            wait()
+            c.fwd()
+            wait()
+            c.bwd()
+            wait()
+            for to, t in zip(results[step], (c.out, c.lse, *c.grads)):
+                to.copy_(t)
+
+    chain(torch.cuda.synchronize)
+    want = [[t.clone() for t in r] for r in results]
+
+    def check():
+        torch.cuda.synchronize()
+        assert int(c.status) == 0
+        for got, ref in zip(results, want):
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
+            for t in got:
+                t.fill_(7.0)
+
+    check()
+    for _ in range(10):
+        chain(lambda: None)
+        check()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        chain(lambda: None)
+    for _ in range(10):
+        graph.replay()
+        check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_arrays_of_almost_2_to_31_elements(d):
     """Rows whose byte offsets (and, for 64-bit reads of the arrays, element offsets) are near the
     largest allowed.  Only the first and the last 64 queries have an upstream gradient, so dK and dV
