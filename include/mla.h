@@ -507,7 +507,8 @@ mla_status mla_out_proj(const mla_config* cfg, const void* o_lat, const void* w_
  *   attention follows.  On CUDA cores the result is that of the call on the ring that
  *   mla_cache_read_q4 gives, bit for bit.  On the tensor cores (whichever kernel_path names them)
  *   the operands are fp16, which holds the ring's values exactly and rounds the rest to 2^-11 of
- *   itself: the chunk's latents beyond 65504 are taken as 65504, below 2^-14 to 2^-25.
+ *   itself: the chunk's contents and its rotated positional values are held within +-65504, and
+ *   below 2^-14 they are off by up to 2^-25.
  *   Workspace: mla_attention_q4_workspace_bytes (0 for a bad configuration), 256-byte aligned; it
  *   holds the attended slots as 16-bit or T values for the length of the call, so one serves every
  *   layer.

@@ -276,6 +276,50 @@ def test_chunk_latents_beyond_fp16():
     assert torch.equal(outs[1], outs[2])
 
 
+@pytest.mark.parametrize("d_c,d_rope", [(192, 32), (256, 32)])
+def test_chunk_values_beyond_fp16_are_taken_as_its_limits(d_c, d_rope):
+    """Contents and rotated positional values beyond 65504 give the bits that 65504 gives, and the
+    definition's results with such values held at 65504."""
+    cfg = dataclasses.replace(inputs.with_latent_shape(SMALL, d_c, d_rope), n_heads=2)
+    c, q4, plain = _filled(cfg, api.MLA_PATH_AUTO, 1)
+    lat, (q, w_uv) = _chunk(c, 100), _query(c, 101)
+    q = q * 2.0 ** -12
+
+    def call(content, positional):
+        x = lat.clone()
+        x[0, 7, 5], x[0, 9, d_c - 1] = content, -content
+        x[1, 100, d_c:] = 0
+        x[1, 100, d_c::4] = positional             # alone in its pair: rotated to (x cos, x sin)
+        b = rollout.ChunkBuffers(c, q4=True)
+        api.mla_attention_fwd_q4(c, q, x, q4.codes, q4.scales, q4.slot_frame, 3, 3, w_uv, b.o, b.lse,
+                                 b.workspace, b.dev_status)
+        torch.cuda.synchronize()
+        rollout.check_device_status(b)
+        return x, b.o, b.lse
+
+    # every nonzero sine and cosine here is above 1e-4, so from 1e9 on all such values are beyond
+    runs = [call(*v) for v in ((65504.0, 1e9), (1e6, 1e20), (3e38, 3e38))]
+    for _, o, lse in runs[1:]:
+        assert torch.equal(o, runs[0][1]) and torch.equal(lse, runs[0][2])
+    x, o, lse = call(1e6, 1e6)
+    d = oracle.dims_from(cfg)
+    slots = plain.slot_frame.cpu().numpy()
+    for b in range(cfg.batch):
+        pos = np.concatenate([oracle.token_positions([int(t) for t in slots[b][:3]], d),
+                              oracle.token_positions(range(3, 3 + cfg.chunk_frames), d)])
+        rows = np.concatenate([to_np(plain.cache)[b][:3 * cfg.tokens_per_frame], to_np(x)[b]])
+        raw = rows[:, d_c:]
+        k_r = oracle.rope3d(raw, pos, d)
+        size = np.abs(raw)[:, 0::2] + np.abs(raw)[:, 1::2]
+        e_rot = 2.0 ** -20 * np.repeat(size, 2, axis=1)
+        e_k = np.where(np.abs(k_r) - e_rot > 65504, 0, F16 * np.abs(k_r) + e_rot + 2.0 ** -25)
+        out, ls, e_out, e_lse = oracle.latent_attention(
+            to_np(q)[b], np.clip(rows[:, :d_c], -65504, 65504), np.clip(k_r, -65504, 65504),
+            to_np(w_uv), cfg.softmax_scale, np.zeros(q.shape[1:]), e_k, F16 + 1.1e-4, 2.0 ** -25)
+        _within(o.view(*q.shape[:3], -1)[b], out, e_out, 2.0 ** -8)
+        _within(lse[b], ls, e_lse, 0.0)
+
+
 @pytest.mark.parametrize("fuse_uv", [True, False])
 def test_cuda_cores_equal_the_call_on_the_rings_values(fuse_uv):
     c, q4, plain = _filled(SMALL, api.MLA_PATH_SIMT, 5)
