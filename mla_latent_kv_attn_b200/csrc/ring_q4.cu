@@ -127,8 +127,10 @@ __device__ __forceinline__ void decode8(uint32_t codes, uint32_t byte, float (&x
     x[i] = (__uint_as_float(0x4B000000u | ((codes >> (4 * i)) & 15u)) - 8388616.f) * s;
 }
 
-// In the append and the preparation gridDim.y samples take turns, and a sample's pieces (fewer than
-// 2^28) are spread over gridDim.x blocks, one per thread at a time: 32-bit index arithmetic.
+// In the append and the preparation gridDim.y samples take turns, and a sample's pieces are spread
+// over gridDim.x blocks, one per thread at a time.  Ring and chunk hold fewer than 2^31 values each,
+// so the append has fewer than 2^27 pieces, and the preparation, whose pieces are those of both and of
+// up to 254 padding rows of keys, fewer than 2^29 + 2^14: 32-bit index arithmetic.
 
 // Token j of the chunk, group g, goes to ring slot (first_frame + j / tpf) mod W.
 template <typename T>

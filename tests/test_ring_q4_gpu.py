@@ -476,6 +476,41 @@ def test_ring_of_almost_2_to_31_values():
     assert not values[:, :-C * tpf].any()
 
 
+def test_attention_over_a_ring_of_almost_2_to_31_values():
+    """The last frame of the largest ring, whose keys outweigh ten million rows of zeros (each by e^40 or
+    more), against the call on a ring of that frame alone."""
+    cfg = dataclasses.replace(inputs.CONFIGS[1], n_heads=1, frame_h=8, frame_w=8, chunk_frames=1,
+                              window_frames=(2 ** 31 - 1) // (64 * 224))
+    W, tpf, d_c = cfg.window_frames, 64, cfg.d_c
+    lat, last = torch.zeros((2, 1, tpf, cfg.d_latent), device="cuda", dtype=torch.bfloat16)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for x in (lat, last):                                  # (no positional values: no rotation)
+        x[..., :d_c] = torch.randn((1, tpf, d_c), generator=g, device="cuda").bfloat16()
+        x[..., 0] = 8
+    w_uv = _query(api.make_config(cfg), 101)[1]
+    q = torch.zeros((1, tpf, 1, cfg.d_latent), device="cuda", dtype=torch.bfloat16)
+    q[..., :d_c] = torch.randn((1, tpf, 1, d_c), generator=g, device="cuda").bfloat16() / 8
+    q[..., 0] = 8 / cfg.softmax_scale                      # a score of 64 with every other key
+    res = []
+    for c in (cfg, dataclasses.replace(cfg, window_frames=1)):
+        cc = api.make_config(c)
+        ring, buf = rollout.RingQ4(cc), rollout.ChunkBuffers(cc, q4=True)
+        _append(cc, ring, last, W - 1)                     # (slot W - 1, and the one slot)
+        ring.slot_frame.copy_(torch.arange(W - c.window_frames, W, dtype=torch.int32))
+        api.mla_attention_fwd_q4(cc, q, lat, ring.codes, ring.scales, ring.slot_frame,
+                                 c.window_frames, W, w_uv, buf.o, buf.lse, buf.workspace,
+                                 buf.dev_status)
+        torch.cuda.synchronize()
+        rollout.check_device_status(buf)
+        res.append((cc, c, buf, ring))
+    cc, c, _, ring = res[1]
+    out, lse, e_out, e_lse = _reference(cc, c, to_np(ring.read()), ring.slot_frame.cpu().numpy(),
+                                        to_np(lat), to_np(q), np.zeros(q.shape), to_np(w_uv), W, 1)
+    for _, _, buf, _ in res:
+        _within(buf.o.view(1, tpf, 1, -1), out, e_out, 2.0 ** -8)
+        _within(buf.lse, lse, e_lse, 0.0)
+
+
 def test_prefill_on_a_side_stream():
     cfg = SMALL
     c = api.make_config(cfg)
