@@ -550,7 +550,8 @@ mla_status mla_attention_fwd_from_cq_q4(const mla_config* cfg, const void* c_q, 
  * q_row_stride, k_row_stride, v_row_stride: elements from one token to the next of q, k and v (0 =
  * dense: H d_head or H_kv d_head), a multiple of 16 bytes and at least a token's heads; a sample's
  * tokens follow one another (sample stride = tokens * row stride).  So q, k and v may be parts of
- * the rows of one projection's output.  out and every gradient are dense.
+ * the rows of one projection's output, as long as each spans fewer than 2^31 elements with its
+ * strides.  out and every gradient are dense.
  *
  * mla_cross_attention_bwd: the gradients of that call for the upstream gradient d_out (T, dense, as
  * out), given the call's out and lse:

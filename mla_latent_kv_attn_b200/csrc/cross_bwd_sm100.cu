@@ -14,15 +14,18 @@
 // its results (stats -> dK, dV: the statistics; dK, dV -> dQ: only the sums) and once more at its end,
 // so that the end of the last says that all have ended.  One after the other, and with the sums in a
 // launch of their own, the call took 69 us instead of 63.
-// S and dP are computed twice (7 products where 5 would do): a single pass would have to add dQ
-// over blocks, in an order that changes from run to run or in fp32 copies that cost more memory
-// traffic than the two products (115 MB for 4680 queries, 12 heads and 512 states).
+// S and dP are computed twice (7 products where 5 would do): a single pass has to add dQ over the
+// blocks of the state tiles, through atomics in an order that changes from run to run, or in fp32 copies
+// that cost more memory traffic than the two products (115 MB for 4680 queries, 12 heads and 512
+// states).  A cluster per set of up to 8 state tiles could add them in order through shared memory, and
+// up to 128 states need no sum; that kernel is not built.
 // (The statistics inside the dQ kernel, by warps of their own, made that call 75 us instead of 70: the
 // first tiles wait for rows from DRAM.)
-// Measured: 4680 queries, 512 states, 12 heads of 128: 63 us a call (three inputs in turn), 585 TFLOP/s
-// over the five products of the formula and 819 over the seven computed (0.50 of the measured peak),
-// 69 us where every call finds its inputs in memory; batch 4 with mixed lengths 180 to 197 us; batch
-// 2, 1333 queries, up to 333 states, 16 heads of 64 on 4: 34 us.
+// Measured: 4680 queries, 512 states, 12 heads of 128: 62.3 us a call with three inputs in turn (part of
+// them in L2), 591 TFLOP/s over the five products of the formula and 828 over the seven computed (0.50
+// of the measured peak), 68.3 us where every call finds its inputs in memory; batch 4 of these, three
+// inputs in turn, 170 to 216 us by how mixed the lengths are and 242 at full ones; batch 2, 1333 queries,
+// up to 333 states, 16 heads of 64 on 4: 34 us.
 // P and dS are rounded to bf16 as operands (in TMEM); every product accumulates in fp32 in TMEM.
 // Every wait is bounded; one that runs out writes MLA_ERR_DEVICE_TIMEOUT to dev_status.
 #include "cross_tc.cuh"
@@ -945,12 +948,14 @@ __global__ void __launch_bounds__(kThreadsKV, 1)
 }
 
 // Blocks per tile of states.  With a tile for every SM none is shared: dQ fills the SMs that the last
-// tiles leave (4 samples of 4680 queries, 12 heads, 512 states: 178 us against 192 with three blocks
-// per tile at mixed lengths, 247 against 233 at full ones; 2 samples of 2000 queries, 40 heads: 169
-// against 195).  Otherwise, of the counts that give every block at least one query tile, the one whose
-// waves of 148 blocks take the fewest steps (a block costs about three steps beside its query tiles),
-// the smallest on a tie: each more adds sums to write and read.  (Fewer blocks that leave SMs to dQ
-// from the start: 88 us against 63 in one sample; loads of dQ slow the block on the SM beside it.)
+// tiles leave.  That gains at mixed lengths (4 samples of 4680 queries, 12 heads, 512 states: 178 us
+// against 192 with three blocks per tile) and where tiles fill whole rounds (2 samples of 2000 queries,
+// 40 heads: 169 against 195), and loses at full lengths in between (247 against 233: 192 tiles on 148
+// SMs); the host does not know the lengths.  Otherwise, of the counts that give every block at least one
+// query tile, the one whose waves of 148 blocks take the fewest steps (a block costs about three steps
+// beside its query tiles), the smallest on a tie: each more adds sums to write and read.  (Fewer blocks
+// that leave SMs to dQ from the start: 88 us against 63 in one sample; loads of dQ slow the block on the
+// SM beside it.)
 int dkv_splits(int tiles, int work) {
   if (tiles >= 148) return 1;
   int best = 1;

@@ -14,7 +14,10 @@
 // has l, l + 32, ...) and the weights come by shuffles.  A step of 32 rows then waits for memory
 // twice; with the elements over the lanes in both, a butterfly sum per row and four rows in flight
 // bounded these kernels (16 queries against 24 states in fp32: 14.3 us a call, now bound by the
-// launch).  All sums are fp32 and run in a fixed order.
+// launch).  All sums are fp32 and run in a fixed order.  Every warp reads the other side's rows itself,
+// which costs at a layer's size: 4680 queries, 512 states, 12 heads of 128 in fp32 4.2 ms forward and 18.1
+// ms backward (29 GB of keys and values through L2 a forward, whose multiply-adds are 0.2 ms at the CUDA
+// cores' peak); 96 in bf16 2.1 and 8.9 ms, 256 in bf16 6.3 and 26 ms.
 #include <cfloat>
 
 #include "cross.h"

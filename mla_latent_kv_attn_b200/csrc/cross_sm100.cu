@@ -25,9 +25,13 @@
 // States past a sample's length are masked: their scores become -infinity by selection, and their
 // value rows are overwritten with zeros in shared memory (0 * NaN would reach O).
 // Measured: 4680 queries, 512 states, 12 heads of 128: 24.8 us a call, 594 TFLOP/s (0.36 of the measured
-// peak; 2.5 rounds of items, and the products' hand-overs bound each); batch 2, 1333 queries, up to
-// 1501 states, 16 heads of 64 on 4: 42 us, bound by the exponentials (35.5 without them); one query:
-// 9.3 us, the host's side of the call.
+// peak): two rounds of items, one of 148 pairs and one of 148 single tiles; the products' hand-overs
+// bound them, and a pair's round in the steady state takes 11 us.  Batch 8 of these: 139 us at full
+// lengths, 87 to 123 at mixed ones.  Batch 2, 1333 queries, up to 1501 states, 16 heads of 64 on 4:
+// 42 us whatever the shorter sample's length: a round of 148 pairs takes 21 us in the steady state (13
+// of them exponentials, 16 a cycle and SM; XU 51 % and tensor pipe 25 % active over the call), and the
+// 56 single tiles left over, of the longest sample, the rest.  One query: 9.3 us, the host's side of the
+// call.
 #include <cfloat>
 
 #include "cross_tc.cuh"
@@ -615,7 +619,11 @@ mla_status fwd_impl(const CrossDims& d, const CrossArgs& a, cudaStream_t s) {
   p.scale_log2 = d.scale * kLog2e;
   p.kv_len = a.kv_len; p.out = static_cast<bf16*>(a.out); p.lse = a.lse;
   p.dev_status = a.dev_status;
-  // With at least two SMs for every single tile, several share its states.
+  // With at least three SMs for every single tile, several share its states.  In a graph, one query
+  // against 512 and 2048 states: 12 tiles, 8 CTAs each, 6.5 and 9.4 us; 36 tiles, 4 each, 13.9 and 25.0;
+  // 48, 3 each, 15.9 and 29.4; 50, unsplit, 11.2 and 31.4.  So sharing gains at many states and, where
+  // clusters of 3 to 6 do not all find room at once, loses up to 5 us at few.  Two CTAs each for 50 to 74
+  // tiles: 9.5 and 19.6 us, not taken up here.
   if (p.wide == 0 && 3 * p.items <= kSms)
     p.splits = std::min(std::min(kMaxSplits, kSms / p.items), ceil_div(d.n_kv, Sh::kBN));
   if (p.splits > 1) {
