@@ -8,8 +8,9 @@
 // states, whose products take 9 us.)  Roles (384 threads):
 //   warps 0-3, 4-7  softmax of stream 0, 1, one TMEM lane (query row) per thread: online softmax in
 //                 the log2 domain, O rescaled only when a row's maximum grows by more than 2^8; P
-//                 rounded to bf16 (the tensor cores' operand type; the row sum l is taken from the
-//                 unrounded values in fp32); O / l into shared memory, lse
+//                 rounded to bf16 (the type that the product with bf16 V takes: O is off by 2.3e-3 of
+//                 itself, 1.7e-3 by its own rounding; the row sum l is taken from the unrounded values
+//                 in fp32); O / l into shared memory, lse
 //   warp 8        TMA producer: the item's two Q tiles (into the buffer that the item before last
 //                 left), then K_0, V_0, K_1, V_1, ... through a ring of stages
 //   warps 9, 10   MMA issuer of stream 0, 1: S = Q K_j^T (both in shared memory) and
